@@ -1,5 +1,6 @@
 """Per-head latent-KV decode on B200 (sm_100a): a C-ABI CUDA library plus thin
-torch wrappers.  See include/lk.h for the boundary.
+torch wrappers.  See include/lk.h (the latent path) and include/lk_serving.h
+(the serving operators beside it) for the boundary.
 
 The library (liblk.so) is loaded on first use of a wrapper, so the input
 generators (``synth``, ``configs``) import without it; every wrapper still
@@ -11,8 +12,13 @@ _API = ("LatentCache", "LowrankWeight", "device_status", "latent_decode_attn", "
         "rmsnorm_hadamard_quant_i8", "swiglu_quant_i8", "workspaces", "kernel_launches", "dense_decode_attn", "reconstruct_kv",
         "rope_table", "latent_decode_attn_rope", "OutsplitFfn")
 
+_SERVING = ("PagedKVCache", "paged_append", "paged_decode_attn", "paged_evict", "W4Weight", "w4_linear",
+            "rmsnorm_gate_residual")
+
 
 def __getattr__(name):
+    if name in _SERVING:
+        return getattr(importlib.import_module(".serving", __name__), name)
     if name in _API:
         return getattr(importlib.import_module(".api", __name__), name)
     if name == "LkError":
@@ -20,4 +26,4 @@ def __getattr__(name):
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
-__all__ = list(_API) + ["LkError"]
+__all__ = list(_API) + list(_SERVING) + ["LkError"]

@@ -28,6 +28,7 @@ LK_F32, LK_BF16, LK_F16, LK_I8, LK_I4 = 0, 1, 2, 3, 4
 LK_MAX_HEADS = 128
 LK_MAX_RANK = 64
 LK_MAX_HEAD_DIM = 256
+LK_MAX_PAGE_SIZE = 1024
 
 
 class LatentCacheDesc(C.Structure):
@@ -72,6 +73,22 @@ class OutsplitWeightDesc(C.Structure):
     ]
 
 
+class PagedCacheDesc(C.Structure):
+    _fields_ = [
+        ("n_pages", C.c_int32),
+        ("page_size", C.c_int32),
+        ("n_kv_heads", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("dtype", C.c_int),
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("k_scale", C.c_void_p),
+        ("v_scale", C.c_void_p),
+        ("mass", C.c_void_p),
+        ("pos", C.c_void_p),
+    ]
+
+
 class LkError(RuntimeError):
     def __init__(self, status, message):
         super().__init__(f"{message} (status {status})")
@@ -89,6 +106,7 @@ def _load():
     SZ = C.c_size_t
     CP = C.POINTER(LatentCacheDesc)
     WP = C.POINTER(LowrankWeightDesc)
+    KP = C.POINTER(PagedCacheDesc)
     sig = {
         "lk_version": (I32, []),
         "lk_kernel_launches": (C.c_uint64, []),
@@ -123,6 +141,16 @@ def _load():
         "lk_rmsnorm_quant_i8": (C.c_int, [P, C.c_int, I32, I32, C.c_float, P, P, P]),
         "lk_rmsnorm_hadamard_quant_i8": (C.c_int, [P, C.c_int, I32, I32, C.c_float, P, P, P]),
         "lk_swiglu_quant_i8": (C.c_int, [P, P, C.c_int, I32, I32, P, P, P]),
+        "lk_paged_append": (C.c_int, [KP, P, I32, I32, P, P, C.c_int, I32, I32, P, P, P, P, P, P]),
+        "lk_paged_decode_attn": (C.c_int, [KP, P, I32, I32, P, C.c_int, I32, I32, P, I32, C.c_float, I32, P, C.c_int,
+                                           P, SZ, P]),
+        "lk_paged_decode_workspace_bytes": (SZ, [KP, I32, I32, I32, I32]),
+        "lk_paged_evict": (C.c_int, [KP, P, I32, I32, P, P, I32, I32, I32, I32, P, P, P, P, SZ, P]),
+        "lk_paged_evict_workspace_bytes": (SZ, [KP, I32, I32, I32]),
+        "lk_w4_pack": (C.c_int, [P, P, P, P, I32, I32, I32, P, SZ, P]),
+        "lk_w4_packed_bytes": (SZ, [I32, I32, I32, I32]),
+        "lk_w4_linear": (C.c_int, [P, I32, I32, I32, I32, P, C.c_int, I32, I32, P, P, C.c_int, P]),
+        "lk_rmsnorm_gate_residual": (C.c_int, [P, P, P, P, I32, P, C.c_int, I32, I32, C.c_float, C.c_float, P, P, P]),
         "lk_device_status": (C.c_int, [I32]),
     }
     for name, (res, args) in sig.items():

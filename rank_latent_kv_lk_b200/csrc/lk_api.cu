@@ -22,6 +22,8 @@ cudaError_t lk_quant_status_word(unsigned int* value, int reset);
 cudaError_t lk_project_status_word(unsigned int* value, int reset);
 cudaError_t lk_lowrank_status_word(unsigned int* value, int reset);
 cudaError_t lk_gemm_tc_status_word(unsigned int* value, int reset);
+cudaError_t lk_paged_status_word(unsigned int* value, int reset);
+cudaError_t lk_evict_status_word(unsigned int* value, int reset);
 
 namespace {
 
@@ -119,7 +121,7 @@ const char* lk_status_string(lk_status s) {
     case LK_ERR_UNSUPPORTED: return "unsupported";
     case LK_ERR_WORKSPACE: return "workspace too small";
     case LK_ERR_CUDA: return "CUDA error";
-    case LK_ERR_DEVICE: return "device-side bounded wait expired";
+    case LK_ERR_DEVICE: return "a kernel reported an expired wait, or a page or length outside its cache";
   }
   return "unknown status";
 }
@@ -680,7 +682,8 @@ lk_status lk_device_status(int32_t reset) {
   if (e != cudaSuccess) return cuda_fail(e, "lk_device_status");
   cudaError_t (*fns[])(unsigned int*, int) = {lk_decode_status_word, lk_quant_status_word,
                                                lk_project_status_word, lk_lowrank_status_word,
-                                               lk_gemm_tc_status_word};
+                                               lk_gemm_tc_status_word, lk_paged_status_word,
+                                               lk_evict_status_word};
   constexpr int kWords = (int)(sizeof(fns) / sizeof(fns[0]));
   unsigned int words[kWords] = {};
   unsigned int any = 0;
@@ -689,7 +692,9 @@ lk_status lk_device_status(int32_t reset) {
     if (e != cudaSuccess) return cuda_fail(e, "lk_device_status");
     any |= words[i];
   }
-  if (any) return fail(LK_ERR_DEVICE, "device status word 0x%x (a bounded wait expired)", any);
+  // bits of lk_common.cuh: 1, 2 an expired wait; 4, 8 a page or length outside its cache
+  if (any & 3u) return fail(LK_ERR_DEVICE, "device status word 0x%x (a bounded wait expired)", any);
+  if (any) return fail(LK_ERR_DEVICE, "device status word 0x%x (a page or length lies outside its paged cache)", any);
   return LK_OK;
 }
 

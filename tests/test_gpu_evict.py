@@ -1,0 +1,140 @@
+"""Eviction by accumulated attention weight against a sort."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.paged_reference import Pages, evict
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, I8 = torch.bfloat16, torch.float16, torch.int8
+
+
+def expect(pages, next_pos, budget, window, n_sink):
+    """The caches' rows after the call, and the written mass and pos."""
+    names = ["k", "v"] + (["k_scale", "v_scale"] if pages.k_scale is not None else [])
+    want = {n: getattr(pages, n).clone() for n in names + ["mass", "pos"]}
+    page = pages.page
+    for b, n in enumerate(pages.lens):
+        for h in range(pages.kv_heads):
+            src = evict(pages.rows(pages.mass, b, h).numpy(), pages.rows(pages.pos, b, h).numpy(), n, next_pos[b],
+                        budget, window, n_sink)
+            for t, s in enumerate(src):
+                d = (pages.table[b, t // page].item(), h, t % page)
+                f = (pages.table[b, s // page].item(), h, s % page)
+                for x in want:
+                    want[x][d] = getattr(pages, x)[f]
+    return want
+
+
+def compare(pages, cache, want, lens_before, budget):
+    for n, x in want.items():
+        torch.testing.assert_close(getattr(cache, n).cpu(), x, rtol=0, atol=0, equal_nan=True, msg=n)
+
+
+CASES = [
+    # lens, kv heads, dim, page, dtype, budget, window, sinks
+    ([1], 1, 16, 1, BF, 1, 0, 0),
+    ([2, 0, 1], 2, 32, 2, HF, 1, 1, 0),
+    ([100, 64, 65, 3], 2, 64, 16, BF, 64, 8, 4),
+    ([300, 299, 17], 3, 80, 32, HF, 150, 20, 2),
+    ([500], 1, 128, 16, BF, 499, 0, 0),
+    ([500], 1, 128, 16, BF, 1, 0, 0),
+    ([257, 600], 2, 256, 64, I8, 200, 16, 4),
+    ([300], 2, 64, 16, BF, 32, 100, 0),       # more protected than the budget
+    ([5000, 4097], 1, 32, 128, BF, 1000, 64, 4),
+    ([9000], 1, 16, 16, HF, 4500, 0, 1),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
+@pytest.mark.parametrize("kind", ["random", "ties", "special"])
+def test_evict_in_place(case, kind):
+    import rank_latent_kv_lk_b200 as lk
+    lens, hk, dim, page, dt, budget, window, sinks = case
+    pages = Pages(lens, hk, dim, page, dt, seed=budget, mass=True)
+    if kind == "ties":
+        pages.mass = torch.where(pages.live, (pages.mass * 3).floor(), pages.mass)
+    if kind == "special":
+        r = torch.rand(pages.mass.shape, generator=pages.g)
+        m = pages.mass
+        for lo, val in ((0.1, math.inf), (0.2, -math.inf), (0.3, math.nan), (0.4, -0.0), (0.5, 0.0), (0.55, -1.5)):
+            m = torch.where(pages.live & (r < lo) & (r >= lo - 0.1), torch.tensor(val), m)
+        pages.mass = m
+    # positions in no order, as after an earlier eviction
+    for b, n in enumerate(lens):
+        for h in range(hk):
+            perm = torch.randperm(n, generator=pages.g).to(torch.int32)
+            for t in range(n):
+                pages.pos[pages.table[b, t // page], h, t % page] = perm[t]
+    cache, seq = pages.cuda(), pages.seq()
+    nxt = [n + (b % 2) * 5 for b, n in enumerate(lens)]
+    want = expect(pages, nxt, budget, window, sinks)
+    lk.paged_evict(cache, pages.table.cuda(), seq, torch.tensor(nxt, dtype=torch.int32, device="cuda"), max(lens),
+                   budget, window=window, n_sink=sinks)
+    lk.device_status()
+    assert seq.tolist() == [min(n, budget) for n in lens]
+    compare(pages, cache, want, lens, budget)
+
+
+@pytest.mark.parametrize("lens,budget", [([70000], 30000), ([60000, 100], 50000)])
+def test_evict_longer_than_shared_memory(lens, budget):
+    import rank_latent_kv_lk_b200 as lk
+    B, page, dim = len(lens), 512, 16
+    width = -(-max(lens) // page)
+    g = torch.Generator().manual_seed(1)
+    shape = (B * width, 1, page, dim)
+    k = torch.randn(shape, generator=g).to(BF)
+    v = torch.randn(shape, generator=g).to(BF)
+    mass = (torch.rand(shape[:3], generator=g) * 5000).floor()
+    pos = torch.arange(width * page, dtype=torch.int32).repeat(B).view(shape[:3])
+    table = torch.randperm(B * width, generator=g).to(torch.int32).view(B, width)
+    pos[table.flatten().long()] = pos.clone()
+    cache = lk.PagedKVCache.from_tensors(k.cuda(), v.cuda(), None, None, mass.cuda(), pos.cuda())
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out_m, out_p = torch.zeros_like(cache.mass), torch.zeros_like(cache.pos)
+    out_s = torch.zeros_like(seq)
+    lk.paged_evict(cache, table.cuda(), seq, seq + 3, max(lens), budget, window=100, n_sink=4, mass_out=out_m,
+                   pos_out=out_p, seq_len_out=out_s)
+    lk.device_status()
+    assert seq.tolist() == lens and out_s.tolist() == [min(n, budget) for n in lens]
+    assert torch.equal(cache.mass.cpu(), mass) and torch.equal(cache.pos.cpu(), pos)
+    for b, n in enumerate(lens):
+        ids = table[b].long()
+        flat = [x[ids, 0].flatten(0, 1) for x in (mass, pos, k, v)]
+        src = evict(flat[0].numpy(), flat[1].numpy(), n, n + 3, budget, 100, 4)
+        got = [x.cpu()[ids, 0].flatten(0, 1) for x in (out_m, out_p, cache.k, cache.v)]
+        src = torch.from_numpy(np.asarray(src))
+        for x, y in zip(got, flat):
+            assert torch.equal(x[:len(src)], y[src])
+        assert torch.equal(got[2][len(src):], flat[2][len(src):])  # rows moved away from stay
+        assert (got[0][len(src):] == 0).all()
+
+
+def test_evict_skips_and_reports_bad_pages():
+    import rank_latent_kv_lk_b200 as lk
+    pages = Pages([64, 20], 1, 32, 16, BF, seed=2, mass=True)
+    pages.table[0, 1] = pages.n_pages
+    pages.table[0, 3] = -1
+    cache, seq = pages.cuda(), pages.seq()
+    lk.paged_evict(cache, pages.table.cuda(), seq, seq.clone(), 64, 24, window=2)
+    with pytest.raises(lk.LkError):
+        lk.device_status()
+    assert seq.tolist() == [24, 20]
+    for h in range(1):
+        assert torch.equal(pages.rows(cache.k.cpu(), 1, h, 20), pages.rows(pages.k, 1, h, 20))
+
+
+def test_lengths_between_the_calls_of_a_batch():
+    # nothing leaves: lengths equal to and below the budget, none at all
+    import rank_latent_kv_lk_b200 as lk
+    pages = Pages([64, 0, 10], 2, 64, 16, HF, seed=3, mass=True)
+    cache, seq = pages.cuda(), pages.seq()
+    lk.paged_evict(cache, pages.table.cuda(), seq, seq.clone(), 64, 64)
+    lk.paged_evict(cache, pages.table.cuda(), seq, seq.clone(), 64, 1000)
+    lk.device_status()
+    assert seq.tolist() == [64, 0, 10]
+    for n in ("k", "v", "mass", "pos"):
+        torch.testing.assert_close(getattr(cache, n).cpu(), getattr(pages, n), rtol=0, atol=0, equal_nan=True)
