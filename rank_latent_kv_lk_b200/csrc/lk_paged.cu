@@ -15,23 +15,22 @@
 // (maximum, sum, weighted V) in the slot CTA + unit (both only grow along the
 // list, so the slot is its own), and a second kernel joins a unit's partials.
 //
-// Inside a CTA each of the 4 warps takes every fourth block, straight from
-// global memory to registers: 16-byte loads that arrive as operands of
-// m16n8k16 products, so no shared-memory stage and no barrier stand between a
-// load and its use, and the next block's K and V are requested as soon as the
-// current one's registers are free.  Both products have the tokens or the
-// head dim as their 16 rows and 8 heads of the group as their columns:
-//   S^T [16 tokens x 8 heads] = K Q^T: lane (gid, tig) loads dims
-//     32 j + 8 tig .. + 7 of tokens gid and gid + 8.  A product's sum over
-//     dims does not depend on their order, so the eight values serve as they
-//     lie as the k indices {2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9} of two
-//     products, and Q is laid out in shared memory in the same order.
-//   O^T [dims x 8 heads] = V^T P^T: lane (gid, tig) loads dims
-//     64 j + 8 gid .. + 7 of tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9;
-//     one byte-permute per register pairs two tokens of one dim, row gid of
-//     product i being dim 8 gid + 2 i and row gid + 8 dim 8 gid + 2 i + 1.
-//   The weights of S^T become the operand P^T by movmatrix (a transpose of
-//     8 x 8 16-bit values across the warp).
+// Inside a CTA each of the 4 warps takes every fourth block through a ring of
+// its own in shared memory: cp.async (16 bytes a lane) keeps the next blocks'
+// K and V rows in flight while one is computed, and since no other warp
+// touches the ring, no barrier does more than order the lanes.  (Loading the
+// operands straight into registers held 8 KB a warp in flight, and only
+// between a block's products; the ring holds twice that throughout.)  Rows are
+// swizzled (16-byte chunks exclusive-or the row) so that ldmatrix reads eight
+// rows without bank conflicts.  Both products have the tokens or the head dim
+// as their 16 rows and 8 heads of the group as their columns (m16n8k16):
+//   S^T [16 tokens x 8 heads] = K Q^T, K by ldmatrix;
+//   O^T [16 dims x 8 heads] = V^T P^T, V^T by ldmatrix.trans;
+//   the weights of S^T become the operand P^T by movmatrix (a transpose of
+//   8 x 8 16-bit values across the warp).
+// int8 rows go the same way as pairs of bytes: ldmatrix gives a lane four
+// codes of a token (Q is laid out in that order of dims), ldmatrix.trans two
+// dims of two tokens, whose even and odd bytes are the rows of one product.
 // The weights are split into two 16-bit terms (high and remainder), so their
 // rounding is 2^-16 (bf16) or 2^-22 (fp16) relative.  fp16 weights are held
 // 2^14 times larger, which keeps small ones out of the subnormals: the largest
@@ -43,7 +42,9 @@
 // scale over a running power of two, so that they too stay at most 2^14.
 //
 // Masked slots (behind the length, or on a page outside the pool) are not
-// read: their K and V registers are zero and their score is -infinity.
+// read: their K and V are zero-filled and their score is -infinity.
+#include <atomic>
+
 #include "lk_serving.cuh"
 
 namespace {
@@ -115,28 +116,60 @@ LK_DEVICE int seq_blocks(const PagedParams& p, int b) {
   return (len + kTok - 1) / kTok;
 }
 
+LK_DEVICE void cp_async16_zfill(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+LK_DEVICE void cp_async4_zfill(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+template <bool TRANS>
+LK_DEVICE void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Head dims up to 64 VC, 8 NT heads.
 template <int VC, int NT, int DT>
 struct Shape {
-  static constexpr int kKDims = DT == DT_I8 ? 64 : 32;       // dims of a K chunk (16 bytes a lane, 4 lanes a row)
-  static constexpr int kKCh = VC * 64 / kKDims;
-  static constexpr int kVDims = DT == DT_I8 && VC % 2 == 0 ? 16 : 8;  // dims a lane holds of a V chunk
-  static constexpr int kVCh = VC * 8 / kVDims;
-  static constexpr int kVRegs = (DT == DT_I8 ? kVDims : 2 * kVDims) / 4;
-  static constexpr int kMT = VC * 4;                         // products of 16 dims
+  static constexpr int kCh = VC * 64 * (DT == DT_I8 ? 1 : 2) / 16;  // 16-byte chunks of a row
+  static constexpr int kRowB = kCh * 16;
+  static constexpr int kScaleB = DT == DT_I8 ? 2 * kTok * 4 : 0;
+  static constexpr int kStageB = 2 * kTok * kRowB + kScaleB;        // K rows, V rows, scales
+  static constexpr int kSteps = VC * 4;                              // products of 16 dims
   static constexpr int kHP = 8 * NT;
   static constexpr int kOStride = VC * 64 + 4;
-  static constexpr int kQVec = (DT == DT_I8 ? 2 : 1) * kKCh;  // uint4 a lane and 8 heads
-  // registers a lane: accumulators, K and V in flight, and about 70 besides
-  static constexpr int kRegs = 16 * VC * NT + (DT == DT_I8 ? 16 : 32) * VC + 64;
-  static constexpr int kMinCtas = kRegs <= 128 ? 4 : (kRegs <= 168 ? 3 : 2);
+  static constexpr int kRowsPer = 32 / kCh;                          // rows a warp copies at a time
+  // Stages and CTAs an SM: about 64 KB (small rows) to 100 KB of ring a CTA
+  static constexpr int kStages = kStageB <= 6400 ? 4 : (kStageB <= 9000 ? 3 : (kStageB <= 12288 ? 2 : 3));
+  static constexpr int kRingB = kStages * kStageB;
+  static constexpr int kMinCtas = kRingB * kWarps <= 36 * 1024 ? 4 : (kRingB * kWarps <= 68 * 1024 ? 3 : (kRingB * kWarps <= 104 * 1024 ? 2 : 1));
+  static constexpr int kQB = NT * (kSteps / 2) * 32 * 16;
+  static constexpr int kSmem = kWarps * kRingB + kQB;
+  static_assert(kHP * kOStride * 4 <= kRingB, "a warp's partial fits in its ring");
+  static_assert(kStages <= 4, "live masks of the stages fit in 64 bits");
 };
+
+// Exclusive-or of a row's chunk index: eight consecutive rows of one chunk
+// fall in distinct banks for rows of a multiple of 128 bytes, and of 64.
+template <int CH>
+LK_DEVICE int swizzle(int row) {
+  return CH % 8 == 0 ? row & 7 : (row >> 1) & 3;
+}
 
 template <int VC, int NT, int DT>
 __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
     paged_decode_kernel(const __grid_constant__ PagedParams p) {
   using S = Shape<VC, NT, DT>;
-  __shared__ uint4 Qs[NT][S::kQVec][32];
-  __shared__ float ost[kWarps][S::kHP][S::kOStride];
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint4 (*Qs)[S::kSteps / 2][32] = reinterpret_cast<uint4 (*)[S::kSteps / 2][32]>(smem + kWarps * S::kRingB);
   __shared__ float mst[kWarps][S::kHP][2];
   __shared__ float qf[S::kHP];
   __shared__ int sh[4];  // sequence, its first block, blocks in all, blocks of this sequence
@@ -145,6 +178,8 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
   const int gid = lane >> 2, tig = lane & 3;
   const int D = p.D, rows_b = DT == DT_I8 ? D : 2 * D;
   const int per_seq = p.n_kv * p.nch;
+  uint8_t* ring = smem + warp * S::kRingB;
+  const uint32_t ring_a = lk_smem_addr(ring);
   lk_grid_dep_wait();
   lk_grid_dep_launch();
 
@@ -216,40 +251,44 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
       const int t = blk * kTok + (lane & 15);
       return blk < s1 && t < len ? lk_paged_row(page, t, h, p.n_pages, p.n_kv, p.page_shift) : -1;
     };
-    uint32_t kr[2][S::kKCh][4], vr[4][S::kVCh][S::kVRegs];
-    float sc = 0.0f;  // int8: K scale of token l (l < 16) or V scale of token l - 16
-    auto load_k = [&](int row) {
+    // copies a block's rows into a stage; lane l holds the row of token l % 16
+    const int c_row = lane / S::kCh, c_ch = lane - c_row * S::kCh;
+    const bool c_in = c_row < S::kRowsPer;
+    auto issue = [&](int stage, int row) {
+      const uint32_t st = ring_a + stage * S::kStageB;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = __shfl_sync(0xffffffffu, row, gid + 8 * i);
-        const uint8_t* base = p.k + (int64_t)r * rows_b;
-#pragma unroll
-        for (int j = 0; j < S::kKCh; ++j) {
-          const int off = 64 * j + 16 * tig;
-          lk_ldcg16(kr[i][j], base + off, r >= 0 && off < rows_b);
+      for (int i = 0; i < kTok / S::kRowsPer; ++i) {
+        const int t = i * S::kRowsPer + (c_in ? c_row : 0);
+        const int r = __shfl_sync(0xffffffffu, row, t);
+        const bool live = r >= 0 && 16 * c_ch < rows_b;
+        const int64_t off = live ? (int64_t)r * rows_b + 16 * c_ch : 0;
+        const uint32_t dst = st + t * S::kRowB + ((c_ch ^ swizzle<S::kCh>(t)) << 4);
+        if (S::kRowsPer * S::kCh == 32 || c_in) {
+          cp_async16_zfill(dst, p.k + off, live);
+          cp_async16_zfill(dst + kTok * S::kRowB, p.v + off, live);
         }
       }
-      if constexpr (DT == DT_I8) sc = row >= 0 ? __ldcg((lane < 16 ? p.ks : p.vs) + row) : 0.0f;
-    };
-    auto load_v = [&](int row) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = __shfl_sync(0xffffffffu, row, 2 * tig + (i & 1) + 8 * (i >> 1));
-        const uint8_t* base = p.v + (int64_t)r * rows_b;
-#pragma unroll
-        for (int j = 0; j < S::kVCh; ++j) {
-          const int off = (8 * j + gid) * (4 * S::kVRegs);
-          if constexpr (S::kVRegs == 4) lk_ldcg16(vr[i][j], base + off, r >= 0 && off < rows_b);
-          else lk_ldcg8(vr[i][j], base + off, r >= 0 && off < rows_b);
-        }
+      if constexpr (DT == DT_I8) {
+        const float* src = lane < 16 ? p.ks : p.vs;
+        cp_async4_zfill(st + 2 * kTok * S::kRowB + 4 * lane, src + max(row, 0), row >= 0);
       }
     };
 
-    int blk = s0 + warp;
-    int row = row_of(blk, page_of(blk));
-    load_k(row);
-    load_v(row);
-    int page_next = page_of(blk + kWarps);
+    int blk = s0 + warp, stage = 0, page_next;
+    uint64_t live_bits = 0;  // 16 bits a stage in flight, the next to be computed lowest
+    {
+      int pages[S::kStages];
+#pragma unroll
+      for (int i = 0; i < S::kStages; ++i) pages[i] = page_of(blk + i * kWarps);
+#pragma unroll
+      for (int i = 0; i < S::kStages - 1; ++i) {
+        const int row = row_of(blk + i * kWarps, pages[i]);
+        live_bits |= (uint64_t)(__ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu) << (16 * i);
+        if (blk + i * kWarps < s1) issue(i, row);
+        lk_cp_async_commit();
+      }
+      page_next = pages[S::kStages - 1];
+    }
 
     // ---- the group's queries, in the order of the K registers
     if constexpr (DT == DT_I8) {
@@ -268,32 +307,32 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
       }
       __syncthreads();
     }
-    for (int i = threadIdx.x; i < NT * S::kQVec * 32; i += kThreads) {
-      const int l = i & 31, x = i >> 5, nt = x / S::kQVec, v = x - nt * S::kQVec;
-      const int j = nt * 8 + (l >> 2);
-      const int dim = DT == DT_I8 ? 64 * (v >> 1) + 16 * (l & 3) + 8 * (v & 1) : 32 * v + 8 * (l & 3);
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (j < heads && dim < D) {
-        w = __ldcg(reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_stride +
-                                                  (int64_t)(h * p.group + n0 + j) * D + dim));
+    for (int i = threadIdx.x; i < NT * S::kSteps * 32; i += kThreads) {
+      // one product's two registers: 16-bit dims 2 tig, + 1, 2 tig + 8, + 9; int8 dims 4 tig .. 4 tig + 3
+      const int l = i & 31, x = i >> 5, nt = x / S::kSteps, st = x - nt * S::kSteps;
+      const int j = nt * 8 + (l >> 2), t4 = l & 3;
+      const int d0 = 16 * st + (DT == DT_I8 ? 4 * t4 : 2 * t4), d1 = d0 + (DT == DT_I8 ? 2 : 8);
+      uint32_t w[2] = {0, 0};
+      if (j < heads && 16 * st < D) {
+        const uint16_t* src = p.q + (int64_t)b * p.q_stride + (int64_t)(h * p.group + n0 + j) * D;
+        w[0] = __ldcg(reinterpret_cast<const uint32_t*>(src + d0));
+        w[1] = __ldcg(reinterpret_cast<const uint32_t*>(src + d1));
         if (DT == DT_I8 && !p.q_f16) {
           const float f = qf[j];
-          w.x = lk_pack_f16x2(lk_bf16lo(w.x) * f, lk_bf16hi(w.x) * f);
-          w.y = lk_pack_f16x2(lk_bf16lo(w.y) * f, lk_bf16hi(w.y) * f);
-          w.z = lk_pack_f16x2(lk_bf16lo(w.z) * f, lk_bf16hi(w.z) * f);
-          w.w = lk_pack_f16x2(lk_bf16lo(w.w) * f, lk_bf16hi(w.w) * f);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) w[e] = lk_pack_f16x2(lk_bf16lo(w[e]) * f, lk_bf16hi(w[e]) * f);
         }
       }
-      Qs[nt][v][l] = w;
+      reinterpret_cast<uint2*>(&Qs[nt][st >> 1][l])[st & 1] = make_uint2(w[0], w[1]);
     }
     __syncthreads();
 
-    float o[S::kMT][NT][4], m[NT][2], l[NT][2], sf[NT][2];
+    float o[S::kSteps][NT][4], m[NT][2], l[NT][2], sf[NT][2];
     float vref = 0.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < S::kMT; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
+      for (int i = 0; i < S::kSteps; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = 8 * nt + 2 * tig + e;
@@ -304,47 +343,66 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
       }
     }
 
+    const int f_row = (lane & 7) + (lane & 8);  // ldmatrix: this lane's row and chunk of a pair
+    const uint32_t f_at = f_row * S::kRowB;
+    const uint32_t f_ch = ((lane >> 4) ^ swizzle<S::kCh>(f_row)) << 4;
     for (; blk < s1; blk += kWarps) {
+      // ---- request the block S::kStages - 1 ahead, then wait for this one
+      {
+        const int ahead = blk + (S::kStages - 1) * kWarps;
+        const int row = row_of(ahead, page_next);
+        page_next = page_of(ahead + kWarps);
+        live_bits |= (uint64_t)(__ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu) << (16 * (S::kStages - 1));
+        if (ahead < s1) issue(stage == 0 ? S::kStages - 1 : stage - 1, row);
+        lk_cp_async_commit();
+      }
+      lk_cp_async_wait<S::kStages - 1>();
+      __syncwarp();
+      const uint32_t live = (uint32_t)live_bits & 0xFFFFu;
+      live_bits >>= 16;
+      const uint32_t st = ring_a + stage * S::kStageB;
+
       // ---- scores of 16 tokens
       float c[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < S::kKCh; ++j) {
-        if constexpr (DT == DT_I8) {
+      for (int v = 0; v < S::kSteps / 2; ++v) {
+        uint4 qv[NT];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x = kr[0][j][i] ^ 0x80808080u, y = kr[1][j][i] ^ 0x80808080u;
+        for (int nt = 0; nt < NT; ++nt) qv[nt] = Qs[nt][v][lane];
+        if constexpr (DT == DT_I8) {
+          uint32_t k4[4];
+          ldmatrix4<false>(k4, st + f_at + (f_ch ^ (v << 5)));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t x = k4[2 * i] ^ 0x80808080u, y = k4[2 * i + 1] ^ 0x80808080u;
             const uint32_t a0 = codes_f16<0x4140>(x), a2 = codes_f16<0x4342>(x);
             const uint32_t a1 = codes_f16<0x4140>(y), a3 = codes_f16<0x4342>(y);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 qv = reinterpret_cast<const uint2*>(&Qs[nt][2 * j + (i >> 1)][lane])[i & 1];
-              mma16816<DT>(c[nt], a0, a1, a2, a3, qv.x, qv.y);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<DT>(c[nt], a0, a1, a2, a3, i ? qv[nt].z : qv[nt].x, i ? qv[nt].w : qv[nt].y);
           }
         } else {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint4 qv = Qs[nt][j][lane];
-            mma16816<DT>(c[nt], kr[0][j][0], kr[1][j][0], kr[0][j][1], kr[1][j][1], qv.x, qv.y);
-            mma16816<DT>(c[nt], kr[0][j][2], kr[1][j][2], kr[0][j][3], kr[1][j][3], qv.z, qv.w);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t k4[4];
+            ldmatrix4<false>(k4, st + f_at + (f_ch ^ ((2 * v + i) << 5)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<DT>(c[nt], k4[0], k4[1], k4[2], k4[3], i ? qv[nt].z : qv[nt].x, i ? qv[nt].w : qv[nt].y);
           }
         }
       }
-      const bool live0 = __shfl_sync(0xffffffffu, row, gid) >= 0;
-      const bool live1 = __shfl_sync(0xffffffffu, row, gid + 8) >= 0;
+      const bool live0 = (live >> gid) & 1, live1 = (live >> (gid + 8)) & 1;
       float ks0 = 1.0f, ks1 = 1.0f, vs0 = 1.0f, vs1 = 1.0f;
       if constexpr (DT == DT_I8) {
-        ks0 = __shfl_sync(0xffffffffu, sc, gid);
-        ks1 = __shfl_sync(0xffffffffu, sc, gid + 8);
-        vs0 = __shfl_sync(0xffffffffu, sc, gid + 16);
-        vs1 = __shfl_sync(0xffffffffu, sc, gid + 24);
+        const float* sc = reinterpret_cast<const float*>(ring + stage * S::kStageB + 2 * kTok * S::kRowB);
+        ks0 = sc[gid];
+        ks1 = sc[gid + 8];
+        vs0 = sc[gid + 16];
+        vs1 = sc[gid + 24];
       }
-      // ---- the next block's K
-      const int row_next = row_of(blk + kWarps, page_next);
-      page_next = page_of(blk + 2 * kWarps);
-      load_k(row_next);
 
       // ---- running maximum and weights
       float alpha[NT][2];
@@ -407,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
         for (int nt = 0; nt < NT; ++nt) {
           const float f0 = alpha[nt][0] * grow, f1 = alpha[nt][1] * grow;
 #pragma unroll
-          for (int i = 0; i < S::kMT; ++i) {
+          for (int i = 0; i < S::kSteps; ++i) {
             o[i][nt][0] *= f0;
             o[i][nt][1] *= f1;
             o[i][nt][2] *= f0;
@@ -434,44 +492,40 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
 
       // ---- weighted V
 #pragma unroll
-      for (int j = 0; j < S::kVCh; ++j) {
+      for (int v = 0; v < S::kCh / 2; ++v) {
+        uint32_t v4[4];
+        ldmatrix4<true>(v4, st + kTok * S::kRowB + f_at + (f_ch ^ (v << 5)));
+        if constexpr (DT == DT_I8) {
 #pragma unroll
-        for (int w = 0; w < S::kVRegs; ++w) {
-          if constexpr (DT == DT_I8) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              // dims 4 w + 2 half, + 1 of token pairs (0, 1) and (2, 3): [t0 d, t1 d, t0 d + 1, t1 d + 1]
-              const uint32_t sel = half ? 0x7362u : 0x5140u;
-              const uint32_t x = __byte_perm(vr[0][j][w], vr[1][j][w], sel) ^ 0x80808080u;
-              const uint32_t y = __byte_perm(vr[2][j][w], vr[3][j][w], sel) ^ 0x80808080u;
-              const uint32_t a0 = codes_f16<0x4140>(x), a1 = codes_f16<0x4342>(x);
-              const uint32_t a2 = codes_f16<0x4140>(y), a3 = codes_f16<0x4342>(y);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float (&acc)[4] = o[j * (S::kVDims / 2) + 2 * w + half][nt];
-                mma16816<DT>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                mma16816<DT>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-              }
-            }
-          } else {
-            const uint32_t a0 = __byte_perm(vr[0][j][w], vr[1][j][w], 0x5410);
-            const uint32_t a1 = __byte_perm(vr[0][j][w], vr[1][j][w], 0x7632);
-            const uint32_t a2 = __byte_perm(vr[2][j][w], vr[3][j][w], 0x5410);
-            const uint32_t a3 = __byte_perm(vr[2][j][w], vr[3][j][w], 0x7632);
+          for (int i = 0; i < 2; ++i) {
+            // bytes: token 2 tig dims 2 gid, + 1, then token 2 tig + 1
+            const uint32_t x = v4[2 * i] ^ 0x80808080u, y = v4[2 * i + 1] ^ 0x80808080u;
+            const uint32_t a0 = codes_f16<0x4240>(x), a1 = codes_f16<0x4341>(x);
+            const uint32_t a2 = codes_f16<0x4240>(y), a3 = codes_f16<0x4341>(y);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float (&acc)[4] = o[j * 4 + w][nt];
+              float (&acc)[4] = o[2 * v + i][nt];
               mma16816<DT>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
               mma16816<DT>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
             }
           }
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float (&acc)[4] = o[v][nt];
+            mma16816<DT>(acc, v4[0], v4[2], v4[1], v4[3], ph[nt][0], ph[nt][1]);
+            mma16816<DT>(acc, v4[0], v4[2], v4[1], v4[3], pl[nt][0], pl[nt][1]);
+          }
         }
       }
-      load_v(row_next);
-      row = row_next;
+      __syncwarp();  // the stage is read: the next request may fill it
+      if (++stage == S::kStages) stage = 0;
     }
 
-    // ---- the warps' states, then the segment's partial
+    // ---- the warps' states (in the drained ring), then the segment's partial
+    lk_cp_async_wait<0>();
+    __syncwarp();
+    float* ost = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -488,11 +542,11 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
         if (j < heads) {
           const float f = DT == DT_I8 ? vref : 1.0f;
 #pragma unroll
-          for (int i = 0; i < S::kMT; ++i) {
-            constexpr int kPer = S::kVDims / 2;
-            const int dim = (i / kPer) * 8 * S::kVDims + S::kVDims * gid + 2 * (i % kPer);
-            ost[warp][j][dim] = o[i][nt][e] * f;
-            ost[warp][j][dim + 1] = o[i][nt][2 + e] * f;
+          for (int i = 0; i < S::kSteps; ++i) {
+            // rows gid and gid + 8 of a product: 16-bit dims gid, gid + 8, int8 dims 2 gid, 2 gid + 1
+            const int d0 = 16 * i + (DT == DT_I8 ? 2 * gid : gid), d1 = d0 + (DT == DT_I8 ? 1 : 8);
+            ost[j * S::kOStride + d0] = o[i][nt][e] * f;
+            ost[j * S::kOStride + d1] = o[i][nt][2 + e] * f;
           }
         }
       }
@@ -510,7 +564,8 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
       for (int w = 0; w < kWarps; ++w) {
         // a warp without a live token has weight 0 (and the sum 0)
         const float f = mst[w][j][0] == -INFINITY ? 0.0f : exp2f(mst[w][j][0] - M);
-        const float4 x = *reinterpret_cast<const float4*>(&ost[w][j][d]);
+        const float4 x = *reinterpret_cast<const float4*>(
+            reinterpret_cast<const float*>(smem + w * S::kRingB) + j * S::kOStride + d);
         acc.x = fmaf(f, x.x, acc.x);
         acc.y = fmaf(f, x.y, acc.y);
         acc.z = fmaf(f, x.z, acc.z);
@@ -533,9 +588,11 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
 // CTAs [0, batch * n_heads): one (sequence, head) each: its pieces' weights,
 // then out = sum_c w_c O_c / sum_c w_c l_c, the pieces dealt out to groups of
 // D / 4 threads.  CTAs behind them (accumulate): kMassTok slots of one
-// (sequence, kv head): mass += sum over the heads of exp2(s - M) / L.
+// (sequence, kv head), four a thread: mass += sum over the heads of
+// exp2(s - M) / L.  Latency-bound: what does not depend on the statistics
+// (pieces, scores, page table, mass) is requested before they are reduced.
 constexpr int kJoinThreads = 256;
-constexpr int kMassTok = 1024;
+constexpr int kMassTok = 4 * kJoinThreads;
 
 struct JoinParams {
   const int32_t* starts;
@@ -563,7 +620,8 @@ LK_DEVICE Pieces unit_pieces(const JoinParams& p, int64_t start, int nb, int64_t
   return r;
 }
 
-// Maximum and sum of one head over a unit's pieces (one warp; every lane gets both).
+// Maximum and sum of one head over a unit's pieces (one warp; every lane gets
+// both).  NaN sums stay NaN; a maximum of -infinity has the sum 0.
 LK_DEVICE float2 warp_stats(const JoinParams& p, const Pieces& pc, int unit, int j) {
   const int lane = threadIdx.x & 31;
   float M = -INFINITY, L = 0.0f;
@@ -582,22 +640,21 @@ LK_DEVICE float2 warp_stats(const JoinParams& p, const Pieces& pc, int unit, int
 }
 
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ JoinParams p) {
-  __shared__ float red[kJoinThreads * 4];
+  __shared__ float4 red[kJoinThreads];
   __shared__ float2 st[LK_MAX_HEADS];
   const int per_seq = p.n_kv * p.nch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_heads = p.n_kv * p.group;
   lk_grid_dep_wait();
   lk_grid_dep_launch();
-  const int64_t N = (int64_t)__ldcg(p.starts + p.batch) * per_seq;
   const int n_out = p.batch * n_heads;
   if ((int)blockIdx.x < n_out) {
     const int b = blockIdx.x / n_heads, j = blockIdx.x - b * n_heads;
+    const int64_t N = (int64_t)__ldcg(p.starts + p.batch) * per_seq;
+    const int b0 = __ldcg(p.starts + b), nb = __ldcg(p.starts + b + 1) - b0;
     const int h = j / p.group, jg = j - h * p.group;
     const int ch = jg / p.hp, jc = jg - ch * p.hp;
     const int hc = h * p.nch + ch, unit = b * per_seq + hc;
-    const int b0 = __ldcg(p.starts + b), nb = __ldcg(p.starts + b + 1) - b0;
-    float* red4 = red;
     const int vec = p.D / 4;                 // float4 columns
     const int groups = kJoinThreads / vec;   // D <= 256: at least 4
     const int g = threadIdx.x / vec, d = threadIdx.x - g * vec;
@@ -605,28 +662,40 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     float inv = 0.0f;
     if (nb > 0) {
       const Pieces pc = unit_pieces(p, (int64_t)b0 * per_seq + (int64_t)hc * nb, nb, N);
+      constexpr int kAhead = 4;
+      float4 x[kAhead];
+      float mc[kAhead];
+      auto load = [&](int c, float4& xv, float& mv) {
+        xv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        mv = -INFINITY;
+        if (g < groups && c <= pc.c1) {
+          const int64_t at = ((int64_t)c + unit) * p.hp + jc;
+          mv = __ldcg(p.stats + at * 2);
+          xv = __ldcg(reinterpret_cast<const float4*>(p.part + at * p.D) + d);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) load(pc.c0 + g + i * groups, x[i], mc[i]);
       const float2 s = warp_stats(p, pc, unit, jc);
       // every score -infinity (L = 0): zeros
       inv = s.y == 0.0f ? 0.0f : 1.0f / s.y;
-      if (g < groups) {
-#pragma unroll 4
-        for (int c = pc.c0 + g; c <= pc.c1; c += groups) {
-          const int64_t at = ((int64_t)c + unit) * p.hp + jc;
-          const float mc = __ldcg(p.stats + at * 2);
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part + at * p.D) + d);
-          const float f = mc == -INFINITY ? 0.0f : exp2f(mc - s.x);
-          acc.x = fmaf(f, x.x, acc.x);
-          acc.y = fmaf(f, x.y, acc.y);
-          acc.z = fmaf(f, x.z, acc.z);
-          acc.w = fmaf(f, x.w, acc.w);
+      for (int c = pc.c0 + g; c <= pc.c1; c += kAhead * groups) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const float f = mc[i] == -INFINITY ? 0.0f : exp2f(mc[i] - s.x);
+          acc.x = fmaf(f, x[i].x, acc.x);
+          acc.y = fmaf(f, x[i].y, acc.y);
+          acc.z = fmaf(f, x[i].z, acc.z);
+          acc.w = fmaf(f, x[i].w, acc.w);
+          load(c + (i + kAhead) * groups, x[i], mc[i]);
         }
       }
     }
-    if (g < groups) reinterpret_cast<float4*>(red4)[g * vec + d] = acc;
+    if (g < groups) red[g * vec + d] = acc;
     __syncthreads();
     if ((int)threadIdx.x < vec) {
       for (int i = 1; i < groups; ++i) {
-        const float4 x = reinterpret_cast<float4*>(red4)[i * vec + d];
+        const float4 x = red[i * vec + d];
         acc.x += x.x;
         acc.y += x.y;
         acc.z += x.z;
@@ -659,31 +728,72 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   const int b = bh / p.n_kv, h = bh - b * p.n_kv;
   const int len = max(0, min(__ldcg(p.seq_len + b), p.max_len));
   if (t0 >= len) return;
+  const int64_t N = (int64_t)__ldcg(p.starts + p.batch) * per_seq;
   const int b0 = __ldcg(p.starts + b), nb = __ldcg(p.starts + b + 1) - b0;
+  // this thread's four slots: their rows, mass and first scores
+  const int t = t0 + 4 * threadIdx.x;
+  const int32_t* trow = p.table + (int64_t)b * p.width;
+  const bool whole = p.page_shift >= 2 && t + 4 <= len;  // four slots of one page, 16-byte aligned
+  int row[4];
+  float4 m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (whole) {
+    row[0] = lk_paged_row(__ldcg(trow + (t >> p.page_shift)), t, h, p.n_pages, p.n_kv, p.page_shift);
+    if (row[0] >= 0) m = __ldcg(reinterpret_cast<const float4*>(p.mass + row[0]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      row[e] = t + e < len ? lk_paged_row(__ldcg(trow + ((t + e) >> p.page_shift)), t + e, h, p.n_pages, p.n_kv,
+                                          p.page_shift)
+                           : -1;
+      if (row[e] >= 0) (&m.x)[e] = __ldcg(p.mass + row[e]);
+    }
+  }
+  // scores of four tokens of head j: t < len lies in a written block, whose 16 tokens are all there
+  auto score = [&](int j) {
+    const int ch = j / p.hp;
+    const float* src = p.scores +
+        (((int64_t)b0 * per_seq + (int64_t)(h * p.nch + ch) * nb + t / kTok) * p.hs + (j - ch * p.hp)) * kTok + t % kTok;
+    return __ldcg(reinterpret_cast<const float4*>(src));
+  };
+  constexpr int kAhead = 4;
+  float4 sc[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (t < len && j < p.group) sc[j] = score(j);
   for (int j = warp; j < p.group; j += kJoinThreads / 32) {
     const int ch = j / p.hp, hc = h * p.nch + ch;
     const Pieces pc = unit_pieces(p, (int64_t)b0 * per_seq + (int64_t)hc * nb, nb, N);
     const float2 s = warp_stats(p, pc, b * per_seq + hc, j - ch * p.hp);
-    // exp2(score - M') / L with the sum's factor taken out of L
+    // exp2(score - M) / L with the sum's factor taken out of L
     if (lane == 0) st[j] = make_float2(s.x == -INFINITY ? 0.0f : s.x, s.y == 0.0f ? 0.0f : exp2f(p.offset) / s.y);
   }
   __syncthreads();
-  const int32_t* trow = p.table + (int64_t)b * p.width;
-  for (int t = t0 + threadIdx.x; t < min(len, t0 + kMassTok); t += kJoinThreads) {
-    const int row = lk_paged_row(__ldcg(trow + (t >> p.page_shift)), t, h, p.n_pages, p.n_kv, p.page_shift);
-    if (row < 0) continue;
-    float add = 0.0f;
-    for (int ch = 0; ch < p.nch; ++ch) {
-      const int heads = min(p.group - ch * p.hp, p.hp);
-      const float* src = p.scores +
-          (((int64_t)b0 * per_seq + (int64_t)(h * p.nch + ch) * nb + t / kTok) * p.hs) * kTok + t % kTok;
-#pragma unroll 4
-      for (int j = 0; j < heads; ++j) {
-        const float2 s = st[ch * p.hp + j];
-        add = fmaf(exp2f(__ldcg(src + j * kTok) - s.x), s.y, add);
+  if (t >= len) return;
+  float4 add = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int j0 = 0; j0 < p.group; j0 += kAhead) {
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int j = j0 + e;
+      if (j < p.group) {
+        const float2 s = st[j];
+        add.x = fmaf(exp2f(sc[e].x - s.x), s.y, add.x);
+        add.y = fmaf(exp2f(sc[e].y - s.x), s.y, add.y);
+        add.z = fmaf(exp2f(sc[e].z - s.x), s.y, add.z);
+        add.w = fmaf(exp2f(sc[e].w - s.x), s.y, add.w);
       }
+      if (j + kAhead < p.group) sc[e] = score(j + kAhead);
     }
-    p.mass[row] = __ldcg(p.mass + row) + add;
+  }
+  m.x += add.x;
+  m.y += add.y;
+  m.z += add.z;
+  m.w += add.w;
+  if (whole) {
+    if (row[0] >= 0) *reinterpret_cast<float4*>(p.mass + row[0]) = m;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (row[e] >= 0) p.mass[row[e]] = (&m.x)[e];
   }
 }
 
@@ -853,11 +963,28 @@ Plan make_plan(int batch, int n_kv, int n_heads, int D, int dtype, int max_len, 
   return r;
 }
 
+// Raises a kernel's dynamic shared memory limit once per device.
+template <int VC, int NT, int DT>
+cudaError_t launch_one(int grid, const PagedParams& p, cudaStream_t stream) {
+  using S = Shape<VC, NT, DT>;
+  static std::atomic<uint64_t> ready{0};  // devices (bit = number mod 64)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(paged_decode_kernel<VC, NT, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return lk::launch_pdl(paged_decode_kernel<VC, NT, DT>, dim3(grid), dim3(kThreads), stream, p, S::kSmem);
+}
+
 template <int VC, int NT>
 cudaError_t launch_split(int dt, int grid, const PagedParams& p, cudaStream_t stream) {
-  if (dt == DT_BF16) return lk::launch_pdl(paged_decode_kernel<VC, NT, DT_BF16>, dim3(grid), dim3(kThreads), stream, p);
-  if (dt == DT_F16) return lk::launch_pdl(paged_decode_kernel<VC, NT, DT_F16>, dim3(grid), dim3(kThreads), stream, p);
-  return lk::launch_pdl(paged_decode_kernel<VC, NT, DT_I8>, dim3(grid), dim3(kThreads), stream, p);
+  if (dt == DT_BF16) return launch_one<VC, NT, DT_BF16>(grid, p, stream);
+  if (dt == DT_F16) return launch_one<VC, NT, DT_F16>(grid, p, stream);
+  return launch_one<VC, NT, DT_I8>(grid, p, stream);
 }
 
 }  // namespace

@@ -36,25 +36,3 @@ LK_DEVICE int lk_paged_row(int page, int slot, int h, int n_pages, int n_kv_head
   }
   return ((page * n_kv_heads + h) << page_shift) | (slot & ((1 << page_shift) - 1));
 }
-
-// Reads of what an earlier kernel of the stream may have written go past L1
-// (ld.global.cg): a kernel started early under programmatic dependent launch
-// must not meet a line that its SM cached before that kernel finished.
-LK_DEVICE void lk_ldcg16(uint32_t (&r)[4], const void* p, bool live) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3])
-      : "l"(p), "r"((uint32_t)live)
-      : "memory");
-}
-LK_DEVICE void lk_ldcg8(uint32_t (&r)[2], const void* p, bool live) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-      "@p ld.global.cg.v2.u32 {%0, %1}, [%2];\n\t}"
-      : "=&r"(r[0]), "=&r"(r[1])
-      : "l"(p), "r"((uint32_t)live)
-      : "memory");
-}
