@@ -33,8 +33,8 @@
 // dims of two tokens, whose even and odd bytes are the rows of one product.
 // The weights are split into two 16-bit terms (high and remainder), so their
 // rounding is 2^-16 (bf16) or 2^-22 (fp16) relative.  fp16 weights are held
-// 2^14 times larger, which keeps small ones out of the subnormals: the largest
-// weight is 2^14 and the smallest step 2^-24.
+// 2^10 times larger, which keeps small ones out of the subnormals: the largest
+// weight is 2^14, the sum at least 2^10 and the smallest step 2^-24.
 // int8 caches: codes are exact in fp16 (byte permute into the mantissa of
 // 1024, one exact subtract); bf16 queries are first scaled by a power of two
 // per head so that the largest lies in [2^14, 2^15) (values below 2^-39 of
@@ -71,6 +71,19 @@ struct PagedParams {
   int n_pages, page_shift, n_kv, D, batch, width, group, nch, max_len, q_stride, q_f16;
   int hs;           // score rows per block
 };
+
+// The reference a head's weights are taken relative to follows the running
+// maximum only once a score lies more than kSlack (log2) above it: the warp
+// then reduces the maximum and rescales, otherwise one vote does.  Weights are
+// so at most 2^kSlack; fp16 ones are held 2^kHeld times larger.
+constexpr float kSlack = 4.0f, kHeld = 10.0f;
+
+// 2^x; results below 2^-126 are 0 (such weights are nothing beside the sum).
+LK_DEVICE float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 LK_DEVICE uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
@@ -116,6 +129,9 @@ LK_DEVICE int seq_blocks(const PagedParams& p, int b) {
   return (len + kTok - 1) / kTok;
 }
 
+LK_DEVICE void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 LK_DEVICE void cp_async16_zfill(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
@@ -274,6 +290,32 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
       }
     };
 
+    // The same for 16 live tokens of one page: their rows are consecutive, so
+    // the addresses are one base and constant steps.
+    const uint32_t c_dst = c_row * S::kRowB + ((c_ch ^ swizzle<S::kCh>(c_row)) << 4);
+    const bool c_live = 16 * c_ch < rows_b;
+    auto issue_page = [&](int stage, int row) {
+      const uint32_t st = ring_a + stage * S::kStageB;
+      const int64_t off = (int64_t)__shfl_sync(0xffffffffu, row, 0) * rows_b + (c_live ? c_row * rows_b + 16 * c_ch : 0);
+      const uint8_t* ks = p.k + off;
+      const uint8_t* vs = p.v + off;
+      if (S::kRowsPer * S::kCh == 32 || c_in) {
+#pragma unroll
+        for (int i = 0; i < kTok / S::kRowsPer; ++i) {
+          const uint32_t dst = st + i * S::kRowsPer * S::kRowB + (c_dst ^ (swizzle<S::kCh>(i * S::kRowsPer) << 4));
+          if (rows_b == S::kRowB) {
+            cp_async16(dst, ks + i * S::kRowsPer * S::kRowB);
+            cp_async16(dst + kTok * S::kRowB, vs + i * S::kRowsPer * S::kRowB);
+          } else {
+            cp_async16_zfill(dst, ks + i * S::kRowsPer * rows_b, c_live);
+            cp_async16_zfill(dst + kTok * S::kRowB, vs + i * S::kRowsPer * rows_b, c_live);
+          }
+        }
+      }
+      if constexpr (DT == DT_I8)
+        cp_async4_zfill(st + 2 * kTok * S::kRowB + 4 * lane, (lane < 16 ? p.ks : p.vs) + row, true);
+    };
+
     int blk = s0 + warp, stage = 0, page_next;
     uint64_t live_bits = 0;  // 16 bits a stage in flight, the next to be computed lowest
     {
@@ -352,8 +394,11 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
         const int ahead = blk + (S::kStages - 1) * kWarps;
         const int row = row_of(ahead, page_next);
         page_next = page_of(ahead + kWarps);
-        live_bits |= (uint64_t)(__ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu) << (16 * (S::kStages - 1));
-        if (ahead < s1) issue(stage == 0 ? S::kStages - 1 : stage - 1, row);
+        const uint32_t live = __ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu;
+        live_bits |= (uint64_t)live << (16 * (S::kStages - 1));
+        const int to = stage == 0 ? S::kStages - 1 : stage - 1;
+        if (live == 0xFFFFu && p.page_shift >= 4) issue_page(to, row);
+        else if (ahead < s1) issue(to, row);
         lk_cp_async_commit();
       }
       lk_cp_async_wait<S::kStages - 1>();
@@ -394,7 +439,6 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
           }
         }
       }
-      const bool live0 = (live >> gid) & 1, live1 = (live >> (gid + 8)) & 1;
       float ks0 = 1.0f, ks1 = 1.0f, vs0 = 1.0f, vs1 = 1.0f;
       if constexpr (DT == DT_I8) {
         const float* sc = reinterpret_cast<const float*>(ring + stage * S::kStageB + 2 * kTok * S::kRowB);
@@ -404,15 +448,18 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
         vs1 = sc[gid + 24];
       }
 
-      // ---- running maximum and weights
-      float alpha[NT][2];
+      // ---- weights relative to a reference near the maximum
       bool moved = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        c[nt][0] = live0 ? c[nt][0] * (sf[nt][0] * ks0) : -INFINITY;
-        c[nt][1] = live0 ? c[nt][1] * (sf[nt][1] * ks0) : -INFINITY;
-        c[nt][2] = live1 ? c[nt][2] * (sf[nt][0] * ks1) : -INFINITY;
-        c[nt][3] = live1 ? c[nt][3] * (sf[nt][1] * ks1) : -INFINITY;
+        c[nt][0] *= sf[nt][0] * ks0;
+        c[nt][1] *= sf[nt][1] * ks0;
+        c[nt][2] *= sf[nt][0] * ks1;
+        c[nt][3] *= sf[nt][1] * ks1;
+        if (live != 0xFFFFu) {
+          if (!((live >> gid) & 1)) c[nt][0] = c[nt][1] = -INFINITY;
+          if (!((live >> (gid + 8)) & 1)) c[nt][2] = c[nt][3] = -INFINITY;
+        }
         if (p.scores) {
           const int64_t g = ((int64_t)b_start * per_seq + (int64_t)hc * nb + blk) * p.hs;
 #pragma unroll
@@ -425,22 +472,36 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
             }
           }
         }
+        moved |= fmaxf(c[nt][0], c[nt][2]) > m[nt][0] + kSlack || fmaxf(c[nt][1], c[nt][3]) > m[nt][1] + kSlack;
+      }
+      float alpha[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) alpha[nt][0] = alpha[nt][1] = 1.0f;
+      moved = __any_sync(0xffffffffu, moved);
+      if (moved) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(c[nt][e], c[nt][2 + e]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m[nt][e], mx);
+            alpha[nt][e] = ex2(m[nt][e] - (mn == -INFINITY ? 0.0f : mn));
+            m[nt][e] = mn;
+            l[nt][e] *= alpha[nt][e];
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(c[nt][e], c[nt][2 + e]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float mn = fmaxf(m[nt][e], mx);
-          const float use = mn == -INFINITY ? 0.0f : mn;
-          alpha[nt][e] = exp2f(m[nt][e] - use);
-          moved |= mn != m[nt][e];
-          m[nt][e] = mn;
-          // fp16 weights are held 2^14 times larger (the sum with them)
-          const float ref = DT == DT_BF16 ? use : use - 14.0f;
-          c[nt][e] = exp2f(c[nt][e] - ref);
-          c[nt][2 + e] = exp2f(c[nt][2 + e] - ref);
-          l[nt][e] = l[nt][e] * alpha[nt][e] + (c[nt][e] + c[nt][2 + e]);
+          const float ref = (m[nt][e] == -INFINITY ? 0.0f : m[nt][e]) - (DT == DT_BF16 ? 0.0f : kHeld);
+          c[nt][e] = ex2(c[nt][e] - ref);
+          c[nt][2 + e] = ex2(c[nt][2 + e] - ref);
+          l[nt][e] += c[nt][e] + c[nt][2 + e];
         }
       }
       float grow = 1.0f;
@@ -450,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
-        if (a > vref) {
+        if (a > vref) {  // the same in every lane
           const float up = __uint_as_float(min((__float_as_uint(a) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
           grow = vref / up;
           vref = up;
@@ -460,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
         vs0 *= inv;
         vs1 *= inv;
       }
-      if (__any_sync(0xffffffffu, moved)) {
+      if (moved) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float f0 = alpha[nt][0] * grow, f1 = alpha[nt][1] * grow;
@@ -563,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         // a warp without a live token has weight 0 (and the sum 0)
-        const float f = mst[w][j][0] == -INFINITY ? 0.0f : exp2f(mst[w][j][0] - M);
+        const float f = mst[w][j][0] == -INFINITY ? 0.0f : ex2(mst[w][j][0] - M);
         const float4 x = *reinterpret_cast<const float4*>(
             reinterpret_cast<const float*>(smem + w * S::kRingB) + j * S::kOStride + d);
         acc.x = fmaf(f, x.x, acc.x);
@@ -629,13 +690,13 @@ LK_DEVICE float2 warp_stats(const JoinParams& p, const Pieces& pc, int unit, int
     const float2 s = __ldcg(reinterpret_cast<const float2*>(p.stats + (((int64_t)c + unit) * p.hp + j) * 2));
     const float mn = fmaxf(M, s.x);
     if (mn != -INFINITY) {
-      L = (M == -INFINITY ? 0.0f : L * exp2f(M - mn)) + (s.x == -INFINITY ? 0.0f : s.y * exp2f(s.x - mn));
+      L = (M == -INFINITY ? 0.0f : L * ex2(M - mn)) + (s.x == -INFINITY ? 0.0f : s.y * ex2(s.x - mn));
       M = mn;
     }
     if (s.y != s.y) L = s.y;
   }
   const float top = lk_warp_max(M);
-  const float part = L != L ? L : (M == -INFINITY ? 0.0f : L * exp2f(M - top));
+  const float part = L != L ? L : (M == -INFINITY ? 0.0f : L * ex2(M - top));
   return make_float2(top, lk_warp_sum(part));
 }
 
@@ -682,7 +743,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
       for (int c = pc.c0 + g; c <= pc.c1; c += kAhead * groups) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          const float f = mc[i] == -INFINITY ? 0.0f : exp2f(mc[i] - s.x);
+          const float f = mc[i] == -INFINITY ? 0.0f : ex2(mc[i] - s.x);
           acc.x = fmaf(f, x[i].x, acc.x);
           acc.y = fmaf(f, x[i].y, acc.y);
           acc.z = fmaf(f, x[i].z, acc.z);
@@ -776,10 +837,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
       const int j = j0 + e;
       if (j < p.group) {
         const float2 s = st[j];
-        add.x = fmaf(exp2f(sc[e].x - s.x), s.y, add.x);
-        add.y = fmaf(exp2f(sc[e].y - s.x), s.y, add.y);
-        add.z = fmaf(exp2f(sc[e].z - s.x), s.y, add.z);
-        add.w = fmaf(exp2f(sc[e].w - s.x), s.y, add.w);
+        add.x = fmaf(ex2(sc[e].x - s.x), s.y, add.x);
+        add.y = fmaf(ex2(sc[e].y - s.x), s.y, add.y);
+        add.z = fmaf(ex2(sc[e].z - s.x), s.y, add.z);
+        add.w = fmaf(ex2(sc[e].w - s.x), s.y, add.w);
       }
       if (j + kAhead < p.group) sc[e] = score(j + kAhead);
     }
@@ -1065,7 +1126,7 @@ cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream)
   j.hp = r.hp;
   j.hs = r.hs;
   j.out_dtype = a.out_dtype;
-  j.offset = dt == DT_BF16 ? 0.0f : 14.0f;
+  j.offset = dt == DT_BF16 ? 0.0f : kHeld;
   j.mass_chunks = a.accumulate ? (a.max_len + kMassTok - 1) / kMassTok : 0;
   const unsigned ctas = (unsigned)(c.batch * a.n_heads) + (unsigned)(c.batch * c.n_kv_heads) * (unsigned)j.mass_chunks;
   return lk::launch_pdl(paged_join_kernel, dim3(ctas), dim3(kJoinThreads), stream, j);

@@ -88,9 +88,9 @@ def attention(pages, q, scale, want_mass=False):
     moves a weight by 2 ds relative (numerator and sum); a weight enters as two
     16-bit terms (2^-16); the T weighted values and the joins are summed in fp32
     (T 2^-23, but no more than 2^-14 for the lengths here).  Terms in fp16 (fp16
-    and int8 caches) also have a smallest step of 2^-24, so a weight held 2^14
-    times larger is off by up to half of it, 2^-39 of the sum, however small it
-    is; an int8 weight is held relative to a power of two at most twice the
+    and int8 caches) also have a smallest step of 2^-24, so a weight held 2^10
+    times larger is off by up to half of it, 2^-35 of the sum (which is at least
+    2^10 as held), however small it is; an int8 weight is held relative to a power of two at most twice the
     largest V scale."""
     B, H, D = q.shape
     group = H // pages.kv_heads
@@ -115,9 +115,9 @@ def attention(pages, q, scale, want_mass=False):
             tol[b, h] = rel * (p @ v.abs())
             if pages.k_scale is not None:
                 vs = pages.rows(pages.v_scale, b, hk).to(F64)
-                tol[b, h] += 2.0 ** -39 * 2 * vs.max() * pages.rows(pages.v, b, hk).to(F64).abs().sum(0)
+                tol[b, h] += 2.0 ** -35 * 2 * vs.max() * pages.rows(pages.v, b, hk).to(F64).abs().sum(0)
             elif pages.dtype is torch.float16:
-                tol[b, h] += 2.0 ** -39 * v.abs().sum(0)
+                tol[b, h] += 2.0 ** -35 * v.abs().sum(0)
             if want_mass:
                 ids = pages.table[b, :-(-n // pages.page)].long()
                 add = torch.zeros(len(ids) * pages.page, dtype=F64)
