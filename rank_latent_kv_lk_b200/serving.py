@@ -5,39 +5,64 @@ weights, and the norms around a block.
 Marshalling only.  What the C ABI cannot see -- a tensor's shape, strides,
 type and device -- is checked here (ValueError, TypeError); the rest is the
 library's (LkError).  Every call runs on its tensors' device and on that
-device's current stream, or on `stream`; scratch memory comes from torch's
-allocator per call, so calls on several streams and captured graphs share none.
+device's current stream, or on `stream`.  Scratch memory is kept per host
+thread and stream, whose calls run one after another; a call that is captured
+into a graph gets its own, from the graph's pool, so replays share none.
 """
 from __future__ import annotations
 
 import ctypes as C
 import math
+import threading
 
 import torch
 
 from ._lib import LK_BF16, LK_F16, LK_F32, LK_I8, PagedCacheDesc, check, lib
 
 _DT = {torch.float32: LK_F32, torch.bfloat16: LK_BF16, torch.float16: LK_F16, torch.int8: LK_I8}
+_FLOAT = {torch.float32: LK_F32, torch.bfloat16: LK_BF16, torch.float16: LK_F16}
+_HALF = {torch.bfloat16: LK_BF16, torch.float16: LK_F16}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+_i32 = torch.int32
 
 
 def _code(dtype, allowed):
-    if dtype not in allowed:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return _DT[dtype]
+    try:
+        return allowed[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype}") from None
 
 
-def _elsewhere(device, stream):
-    """Whether the call has to enter its tensors' device or the given stream first."""
-    return stream is not None or device.index is None or device.index != torch.cuda.current_device()
+class _Scratch(threading.local):
+    """Scratch buffers of this thread's calls, one per stream."""
+
+    def __init__(self):
+        self.buffers = {}
+
+    def get(self, index, stream, nbytes):
+        if _capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+        buf = self.buffers.get((index, stream))
+        if buf is None or buf.numel() < nbytes:
+            # twice what is asked for, so that a growing cache reallocates seldom
+            buf = torch.empty(2 * nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+            self.buffers[index, stream] = buf
+        return buf
 
 
-def _enter(device, stream, fn, *args, **kw):
-    """The call inside its device and stream."""
+_scratch = _Scratch()
+
+
+def _enter(device, stream, fn, *args):
+    """The call inside its tensors' device and the given stream."""
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, not {device}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        return fn(*args, **kw)
+        return fn(*args)
 
 
 def _ptr(t):
@@ -82,7 +107,9 @@ class PagedKVCache:
         return self
 
     def _set(self, k, v, k_scale, v_scale, mass, pos):
-        _code(k.dtype, (torch.bfloat16, torch.float16, torch.int8))
+        _code(k.dtype, _DT)
+        if k.dtype is torch.float32:
+            raise TypeError("a paged cache holds bf16, fp16 or int8")
         if k.dim() != 4 or k.device.type != "cuda":
             raise ValueError("k: a CUDA tensor [n_pages, n_kv_heads, page_size, head_dim] is needed")
         dev, rows = k.device, k.shape[:3]
@@ -99,29 +126,53 @@ class PagedKVCache:
             _same("mass", mass, rows, torch.float32, dev)
             _same("pos", pos, rows, torch.int32, dev)
         self.k, self.v, self.k_scale, self.v_scale, self.mass, self.pos = k, v, k_scale, v_scale, mass, pos
-        self.device, self.dtype, self.rows = dev, k.dtype, rows
+        self.device, self.dtype, self.rows, self.index = dev, k.dtype, rows, dev.index
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self._desc = PagedCacheDesc(self.n_pages, self.page_size, self.n_kv_heads, self.head_dim, _DT[k.dtype],
                                     k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), _ptr(mass), _ptr(pos))
         self._ref = C.byref(self._desc)
+        self._scale = 1.0 / math.sqrt(self.head_dim)
+        self._need = {}
 
     def desc(self):
         return self._ref
 
+    def _decode_bytes(self, batch, heads, max_len, acc):
+        """Workspace of a decode call, asked for once per 1024 tokens of the bound (it grows with it)."""
+        key = (batch, heads, (max_len + 1023) >> 10, acc)
+        need = self._need.get(key)
+        if need is None:
+            need = (lib.lk_paged_decode_workspace_bytes(self._ref, batch, heads, key[2] << 10, acc) or
+                    lib.lk_paged_decode_workspace_bytes(self._ref, batch, heads, max_len, acc))
+            if need:
+                self._need[key] = need
+        return need
+
 
 def _table(cache, page_table, batch):
-    if page_table.dim() != 2 or page_table.shape[0] != batch:
-        raise ValueError(f"page_table: [{batch}, width] is needed, not {tuple(page_table.shape)}")
-    _same("page_table", page_table, page_table.shape, torch.int32, cache.device)
-    return page_table.shape[1]
+    """The page table's width."""
+    shape = page_table.shape
+    if len(shape) != 2 or shape[0] != batch or page_table.dtype is not _i32 or not page_table.is_contiguous() \
+            or page_table.get_device() != cache.index:
+        raise ValueError(f"page_table: a contiguous int32 [{batch}, width] on {cache.device} is needed, not "
+                         f"{page_table.dtype} {tuple(shape)} on {page_table.device}")
+    return shape[1]
+
+
+def _counts(name, t, batch, cache):
+    """An int32 vector of the batch."""
+    if t.dtype is not _i32 or t.shape != (batch,) or not t.is_contiguous() or t.get_device() != cache.index:
+        raise ValueError(f"{name}: a contiguous int32 [{batch}] on {cache.device} is needed, not {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
 
 
 def _new_tokens(cache, name, t):
     """Elements between the tokens of [batch, n_new, n_kv_heads, head_dim]."""
-    if t.dim() != 4 or t.shape[2] != cache.n_kv_heads or t.shape[3] != cache.head_dim or t.device != cache.device:
+    shape = t.shape
+    if len(shape) != 4 or shape[2] != cache.n_kv_heads or shape[3] != cache.head_dim or t.get_device() != cache.index:
         raise ValueError(f"{name}: [batch, n_new, {cache.n_kv_heads}, {cache.head_dim}] on {cache.device} is needed, "
-                         f"not {tuple(t.shape)} on {t.device}")
-    b, n, h, d = t.shape
+                         f"not {tuple(shape)} on {t.device}")
+    b, n, h, d = shape
     sb, sn, sh, sd = t.stride()
     step = sn if n > 1 else (sb if b > 1 else h * d)
     if sd != 1 or (h > 1 and sh != d) or (b > 1 and n > 1 and sb != n * step):
@@ -141,7 +192,7 @@ def paged_append(cache, page_table, k_new, v_new, seq_len, next_pos=None, new_le
     next_pos, the position of each sequence's next token.  The new lengths and
     positions go to seq_len_out / next_pos_out (default: in place).
     """
-    if _elsewhere(cache.device, stream):
+    if stream is not None or cache.index != _current_device():
         return _enter(cache.device, stream, paged_append, cache, page_table, k_new, v_new, seq_len, next_pos, new_len,
                       seq_len_out, next_pos_out)
     step = _new_tokens(cache, "k_new", k_new)
@@ -156,11 +207,12 @@ def paged_append(cache, page_table, k_new, v_new, seq_len, next_pos=None, new_le
     for name, t in (("seq_len", seq_len), ("seq_len_out", seq_len_out), ("next_pos", next_pos),
                     ("next_pos_out", next_pos_out), ("new_len", new_len)):
         if t is not None:
-            _same(name, t, (batch,), torch.int32, cache.device)
-    check(lib.lk_paged_append(cache._ref, page_table.data_ptr(), batch, width, k_new.data_ptr(), v_new.data_ptr(),
-                              _code(k_new.dtype, (torch.bfloat16, torch.float16)), step, n_new, _ptr(new_len),
-                              seq_len.data_ptr(), seq_len_out.data_ptr(), _ptr(next_pos), _ptr(next_pos_out),
-                              _raw_stream(cache.device.index)))
+            _counts(name, t, batch, cache)
+    status = lib.lk_paged_append(cache._ref, page_table.data_ptr(), batch, width, k_new.data_ptr(), v_new.data_ptr(),
+                                 _code(k_new.dtype, _HALF), step, n_new, _ptr(new_len), seq_len.data_ptr(),
+                                 seq_len_out.data_ptr(), _ptr(next_pos), _ptr(next_pos_out), _raw_stream(cache.index))
+    if status:
+        check(status)
 
 
 def paged_decode_attn(cache, page_table, q, seq_len, max_seq_len, softmax_scale=None, accumulate=False, out=None,
@@ -172,31 +224,33 @@ def paged_decode_attn(cache, page_table, q, seq_len, max_seq_len, softmax_scale=
     max_seq_len: host bound.  accumulate: add every cached token's attention
     weight, summed over the heads of its group, to cache.mass.
     """
-    if _elsewhere(cache.device, stream):
+    if stream is not None or cache.index != _current_device():
         return _enter(cache.device, stream, paged_decode_attn, cache, page_table, q, seq_len, max_seq_len,
                       softmax_scale, accumulate, out, out_dtype)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.device != cache.device:
-        raise ValueError(f"q: [batch, n_heads, {cache.head_dim}] on {cache.device} is needed, not {tuple(q.shape)} "
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or q.get_device() != cache.index:
+        raise ValueError(f"q: [batch, n_heads, {cache.head_dim}] on {cache.device} is needed, not {tuple(shape)} "
                          f"on {q.device}")
-    batch, heads, dim = q.shape
-    qs = q.stride()
-    if qs[2] != 1 or (heads > 1 and qs[1] != dim):
-        raise ValueError(f"q: heads must be contiguous within a sequence, strides are {qs}")
+    batch, heads, dim = shape
+    step, inner, one = q.stride()
+    if one != 1 or (heads > 1 and inner != dim):
+        raise ValueError(f"q: heads must be contiguous within a sequence, strides are {q.stride()}")
     width = _table(cache, page_table, batch)
-    _same("seq_len", seq_len, (batch,), torch.int32, cache.device)
+    _counts("seq_len", seq_len, batch, cache)
     if out is None:
-        out = torch.empty((batch, heads, dim), dtype=out_dtype or q.dtype, device=cache.device)
+        out = q.new_empty((batch, heads, dim)) if out_dtype is None else q.new_empty((batch, heads, dim), dtype=out_dtype)
     else:
-        _same("out", out, q.shape, out.dtype, cache.device)
+        _same("out", out, shape, out.dtype, cache.device)
     acc = 1 if accumulate else 0
-    need = lib.lk_paged_decode_workspace_bytes(cache._ref, batch, heads, max_seq_len, acc)
-    ws = torch.empty(need, dtype=torch.uint8, device=cache.device)
-    check(lib.lk_paged_decode_attn(
-        cache._ref, page_table.data_ptr(), batch, width, q.data_ptr(),
-        _code(q.dtype, (torch.bfloat16, torch.float16)), heads, qs[0] if batch > 1 else heads * dim,
-        seq_len.data_ptr(), max_seq_len, 1.0 / math.sqrt(dim) if softmax_scale is None else softmax_scale, acc,
-        out.data_ptr(), _code(out.dtype, (torch.bfloat16, torch.float16, torch.float32)), ws.data_ptr(), need,
-        _raw_stream(cache.device.index)))
+    need = cache._decode_bytes(batch, heads, max_seq_len, acc)
+    raw = _raw_stream(cache.index)
+    status = lib.lk_paged_decode_attn(
+        cache._ref, page_table.data_ptr(), batch, width, q.data_ptr(), _code(q.dtype, _HALF), heads,
+        step if batch > 1 else heads * dim, seq_len.data_ptr(), max_seq_len,
+        cache._scale if softmax_scale is None else softmax_scale, acc, out.data_ptr(), _code(out.dtype, _FLOAT),
+        _scratch.get(cache.index, raw, need).data_ptr(), need, raw)
+    if status:
+        check(status)
     return out
 
 
@@ -210,7 +264,7 @@ def paged_evict(cache, page_table, seq_len, next_pos, max_seq_len, budget, windo
     rows' mass and positions go to mass_out / pos_out and the lengths to
     seq_len_out (default: in place).
     """
-    if _elsewhere(cache.device, stream):
+    if stream is not None or cache.index != _current_device():
         return _enter(cache.device, stream, paged_evict, cache, page_table, seq_len, next_pos, max_seq_len, budget,
                       window, n_sink, mass_out, pos_out, seq_len_out)
     if cache.mass is None:
@@ -226,14 +280,19 @@ def paged_evict(cache, page_table, seq_len, next_pos, max_seq_len, budget, windo
     batch = seq_len.shape[0]
     width = _table(cache, page_table, batch)
     for name, t in (("seq_len", seq_len), ("next_pos", next_pos), ("seq_len_out", seq_len_out)):
-        _same(name, t, (batch,), torch.int32, cache.device)
-    _same("mass_out", mass_out, cache.rows, torch.float32, cache.device)
-    _same("pos_out", pos_out, cache.rows, torch.int32, cache.device)
+        _counts(name, t, batch, cache)
+    if mass_out is not cache.mass:
+        _same("mass_out", mass_out, cache.rows, torch.float32, cache.device)
+    if pos_out is not cache.pos:
+        _same("pos_out", pos_out, cache.rows, torch.int32, cache.device)
     need = lib.lk_paged_evict_workspace_bytes(cache._ref, batch, max_seq_len, budget)
-    ws = torch.empty(need, dtype=torch.uint8, device=cache.device)
-    check(lib.lk_paged_evict(cache._ref, page_table.data_ptr(), batch, width, seq_len.data_ptr(), next_pos.data_ptr(),
-                             max_seq_len, budget, window, n_sink, mass_out.data_ptr(), pos_out.data_ptr(),
-                             seq_len_out.data_ptr(), ws.data_ptr(), need, _raw_stream(cache.device.index)))
+    raw = _raw_stream(cache.index)
+    status = lib.lk_paged_evict(cache._ref, page_table.data_ptr(), batch, width, seq_len.data_ptr(),
+                                next_pos.data_ptr(), max_seq_len, budget, window, n_sink, mass_out.data_ptr(),
+                                pos_out.data_ptr(), seq_len_out.data_ptr(),
+                                _scratch.get(cache.index, raw, need).data_ptr(), need, raw)
+    if status:
+        check(status)
 
 
 class W4Weight:
@@ -252,7 +311,7 @@ class W4Weight:
             raise ValueError(f"{scales.shape[1]} scale groups do not divide {self.k_in} inputs")
         if (up_codes is None) != (up_scales is None):
             raise ValueError("up_codes and up_scales come together")
-        self.gated, self.device = up_codes is not None, dev
+        self.gated, self.device, self.index = up_codes is not None, dev, dev.index
         for name, c, s in (("", codes, scales), ("up_", up_codes, up_scales)):
             if c is not None:
                 _same(name + "codes", c, codes.shape, torch.uint8, dev)
@@ -260,8 +319,9 @@ class W4Weight:
         with torch.cuda.device(dev):
             need = lib.lk_w4_packed_bytes(self.n_out, self.k_in, self.group, int(self.gated))
             self.packed = torch.empty(need, dtype=torch.uint8, device=dev)
+            self.packed_ptr = self.packed.data_ptr()
             check(lib.lk_w4_pack(codes.data_ptr(), scales.data_ptr(), _ptr(up_codes), _ptr(up_scales), self.n_out,
-                                 self.k_in, self.group, self.packed.data_ptr(), need, _raw_stream(dev.index)))
+                                 self.k_in, self.group, self.packed_ptr, need, _raw_stream(dev.index)))
 
 
 def w4_linear(w, x, residual=None, y=None, y_dtype=None, stream=None):
@@ -269,22 +329,26 @@ def w4_linear(w, x, residual=None, y=None, y_dtype=None, stream=None):
 
     x: [m, k_in] bf16 or fp16, rows contiguous; residual: [m, n_out] of x's type.
     """
-    if _elsewhere(w.device, stream):
+    if stream is not None or w.index != _current_device():
         return _enter(w.device, stream, w4_linear, w, x, residual, y, y_dtype)
-    if x.dim() != 2 or x.shape[1] != w.k_in or x.stride(1) != 1 or x.device != w.device:
-        raise ValueError(f"x: [m, {w.k_in}] with contiguous rows on {w.device} is needed, not {tuple(x.shape)} with "
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != w.k_in or x.get_device() != w.index or x.stride(1) != 1:
+        raise ValueError(f"x: [m, {w.k_in}] with contiguous rows on {w.device} is needed, not {tuple(shape)} with "
                          f"strides {x.stride()} on {x.device}")
-    m = x.shape[0]
-    if y is None:
-        y = torch.empty((m, w.n_out), dtype=y_dtype or x.dtype, device=w.device)
-    else:
-        _same("y", y, (m, w.n_out), y.dtype, w.device)
+    m = shape[0]
     if residual is not None:
         _same("residual", residual, (m, w.n_out), x.dtype, w.device)
-    check(lib.lk_w4_linear(w.packed.data_ptr(), w.n_out, w.k_in, w.group, 1 if w.gated else 0, x.data_ptr(),
-                           _code(x.dtype, (torch.bfloat16, torch.float16)), m, x.stride(0) if m > 1 else w.k_in,
-                           _ptr(residual), y.data_ptr(), _code(y.dtype, (torch.bfloat16, torch.float16, torch.float32)),
-                           _raw_stream(w.device.index)))
+    if y is not None:
+        _same("y", y, (m, w.n_out), y.dtype, w.device)
+    elif y_dtype is not None:
+        y = x.new_empty((m, w.n_out), dtype=y_dtype)
+    else:
+        y = x.new_empty((m, w.n_out)) if residual is None else torch.empty_like(residual)
+    status = lib.lk_w4_linear(w.packed_ptr, w.n_out, w.k_in, w.group, w.gated, x.data_ptr(), _code(x.dtype, _HALF), m,
+                              x.stride(0) if m > 1 else w.k_in, None if residual is None else residual.data_ptr(),
+                              y.data_ptr(), _code(y.dtype, _FLOAT), _raw_stream(w.index))
+    if status:
+        check(status)
     return y
 
 
@@ -297,13 +361,13 @@ def rmsnorm_gate_residual(y, x, w_post=None, gate=None, scale=1.0, w_pre=None, e
     y and h may be y.  Returns (x_out, h); h is None without w_pre.
     """
     dev = y.device
-    if _elsewhere(dev, stream):
+    if stream is not None or dev.index is None or dev.index != _current_device():
         return _enter(dev, stream, rmsnorm_gate_residual, y, x, w_post, gate, scale, w_pre, eps, x_out, h)
     dtype = y.dtype
-    code = _code(dtype, (torch.float32, torch.bfloat16, torch.float16))
-    if y.dim() != 2:
-        raise ValueError("y: [m, width] is needed")
+    code = _code(dtype, _FLOAT)
     shape = y.shape
+    if len(shape) != 2:
+        raise ValueError("y: [m, width] is needed")
     m, width = shape
     _same("y", y, shape, dtype, dev)
     _same("x", x, shape, dtype, dev)
@@ -327,6 +391,9 @@ def rmsnorm_gate_residual(y, x, w_post=None, gate=None, scale=1.0, w_pre=None, e
         raise ValueError("h needs w_pre")
     if m == 0:
         return x_out, h
-    check(lib.lk_rmsnorm_gate_residual(y.data_ptr(), x.data_ptr(), _ptr(w_post), _ptr(gate), per_row, _ptr(w_pre),
-                                       code, m, width, scale, eps, x_out.data_ptr(), _ptr(h), _raw_stream(dev.index)))
+    status = lib.lk_rmsnorm_gate_residual(y.data_ptr(), x.data_ptr(), _ptr(w_post), _ptr(gate), per_row, _ptr(w_pre),
+                                          code, m, width, scale, eps, x_out.data_ptr(), _ptr(h),
+                                          _raw_stream(dev.index))
+    if status:
+        check(status)
     return x_out, h
