@@ -45,7 +45,7 @@ struct W4Params {
   const uint16_t* x;
   const uint16_t* residual;
   void* y;
-  int n_out, k_in, steps, tiles, tn, kn, m, x_stride, y_dtype;
+  int n_out, k_in, steps, full_steps, tiles, tn, kn, m, x_stride, y_dtype;
 };
 
 __host__ __device__ constexpr int record_bytes(int group, int mats) { return mats * (1024 + (kStep / group) * 32); }
@@ -85,17 +85,33 @@ LK_DEVICE uint32_t lds4(uint32_t a) {
   return v;
 }
 
-template <bool F16>
-LK_DEVICE uint32_t codes16(uint32_t w, int i) {
-  uint32_t h, r;
-  if constexpr (F16) {
-    h = ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64086408u));
-  } else {
-    h = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x43084308u));
-  }
+// (a & b) | c
+LK_DEVICE uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
+}
+
+// The four registers of a product from a word of codes.  fp16: nibbles 1 and 3
+// are taken where they lie (1024 + 16 n), and a multiply-add brings them down,
+// which saves two shifts; bf16's mantissa has room for the lowest nibble only.
+template <bool F16>
+LK_DEVICE void codes16(uint32_t w, uint32_t (&a)[4]) {
+  if constexpr (F16) {
+    const uint32_t v = w >> 8;
+    const uint32_t h[4] = {and_or(w, 0x000F000Fu, 0x64006400u), and_or(w, 0x00F000F0u, 0x64006400u),
+                           and_or(v, 0x000F000Fu, 0x64006400u), and_or(v, 0x00F000F0u, 0x64006400u)};
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(a[i]) : "r"(h[i]), "r"(0x64086408u));
+      // (1024 + 16 n) / 16 - 72
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(a[i + 1]) : "r"(h[i + 1]), "r"(0x2C002C00u), "r"(0xD480D480u));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(a[i]) : "r"(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u)), "r"(0x43084308u));
+  }
 }
 
 template <bool F16>
@@ -138,17 +154,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
                                          wk * (S::kStages * S::kXStage)
                                    : ring + S::kRec;
   constexpr int kXStep = S::kShared ? S::kXStage : S::kStage;
-  if (!S::kShared && R > 1) {
-    // rows behind the last are zero and stay so
-    for (int i = lane; i < S::kStages * R * 16; i += 32) {
-      const int st = i / (R * 16), r = (i >> 4) % R, c = i & 15;
-      if (r >= rows) {
-        uint4* z = reinterpret_cast<uint4*>(smem + warp * (S::kStages * S::kStage) + st * S::kStage + S::kRec +
-                                            r * kXStride + 16 * c);
-        *z = make_uint4(0, 0, 0, 0);
-      }
-    }
-  }
+  // Rows behind the last are never filled: a column of a product is one row, and theirs are not stored.
   lk_grid_dep_wait();
   lk_grid_dep_launch();
 
@@ -156,6 +162,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
   const uint8_t* src = p.packed + ((int64_t)(mine ? tile : 0) * p.steps + wk) * S::kRec + 16 * lane;
   const int64_t src_step = (int64_t)p.kn * S::kRec;
   int next = wk;
+  // this lane's 16 bytes of x: chunk lane % 16 of every (2 tn)th (its own ring: 2nd) row
+  const int x_c = lane & 15, x_r = (S::kShared ? 2 * wn : 0) + (lane >> 4), x_rows = S::kShared ? 2 * p.tn : 2;
+  const uint16_t* xsrc = p.x + (int64_t)(m0 + min(x_r, rows - 1)) * p.x_stride + 8 * x_c + wk * kStep;
+  const int64_t x_next = (int64_t)x_rows * p.x_stride;
   auto fetch = [&](int stage) {
     if (next < p.steps) {
       if (mine) {
@@ -165,19 +175,22 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
           if (i + 512 <= S::kRec || i + 16 * lane < S::kRec) cp16(dst + i, src + i);
       }
       const uint32_t xd = xbuf + stage * kXStep;
-      if constexpr (S::kShared) {
-        for (int i = wn * 32 + lane; i < R * 16; i += p.tn * 32) {
-          const int r = i >> 4, c = i & 15, k = next * kStep + 8 * c;
-          const bool live = r < rows && k < p.k_in;
-          cp16_zfill(xd + r * kXStride + 16 * c, p.x + (live ? (int64_t)(m0 + r) * p.x_stride + k : 0), live);
+      const uint32_t xl = xd + x_r * kXStride + 16 * x_c;
+      const uint16_t* xs = xsrc;
+      if (next < p.full_steps) {
+        if constexpr (S::kShared) {
+          for (int r = x_r; r < rows; r += x_rows, xs += x_next) cp16(xl + (r - x_r) * kXStride, xs);
+        } else {
+#pragma unroll
+          for (int i = 0; i < (R + 1) / 2; ++i, xs += x_next)
+            if (x_r + 2 * i < rows) cp16(xl + 2 * i * kXStride, xs);
         }
-      } else {
-        for (int i = lane; i < rows * 16; i += 32) {
-          const int r = i >> 4, c = i & 15, k = next * kStep + 8 * c;
-          const bool live = k < p.k_in;
-          cp16_zfill(xd + r * kXStride + 16 * c, p.x + (live ? (int64_t)(m0 + r) * p.x_stride + k : 0), live);
-        }
+      } else {  // inputs end inside the step
+        const bool in = next * kStep + 8 * x_c < p.k_in;
+        for (int r = x_r; r < rows; r += x_rows, xs += x_next)
+          cp16_zfill(xl + (r - x_r) * kXStride, in ? xs : p.x, in);
       }
+      xsrc += p.kn * kStep;
       src += src_step;
       next += p.kn;
     }
@@ -207,7 +220,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
           uint4 xr[MT];
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            xr[t] = R > 1 || gid == 0 ? lds16(xs + t * 8 * kXStride + (2 * c + j) * 64) : make_uint4(0, 0, 0, 0);
+            // one row: all eight columns hold it, and the first is used
+            xr[t] = lds16(xs + t * 8 * kXStride + (2 * c + j) * 64);
           }
 #pragma unroll
           for (int qq = 0; qq < 2; ++qq) {
@@ -217,8 +231,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
 #pragma unroll
             for (int a = 0; a < MATS; ++a) {
               const uint32_t word = q == 0 ? code[a].x : (q == 1 ? code[a].y : (q == 2 ? code[a].z : code[a].w));
-              const uint32_t a0 = codes16<F16>(word, 0), a1 = codes16<F16>(word, 1);
-              const uint32_t a2 = codes16<F16>(word, 2), a3 = codes16<F16>(word, 3);
+              uint32_t A[4];
+              codes16<F16>(word, A);
               float s0 = 0.0f, s1 = 0.0f;
               if (last) {
                 const uint32_t sw = lds4(rec + MATS * 1024 + (a * (kStep / GROUP) + at / GROUP) * 32 + 4 * gid);
@@ -229,9 +243,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
               for (int t = 0; t < MT; ++t) {
                 float (&pt)[4] = part[a][t];
                 const uint32_t b0 = qq ? xr[t].z : xr[t].x, b1 = qq ? xr[t].w : xr[t].y;
-                if (first) mma_first<F16>(pt, a0, a1, a2, a3, b0, b1);
-                else if constexpr (F16) lk_mma_f16_16816(pt, a0, a1, a2, a3, b0, b1);
-                else lk_mma_bf16_16816(pt, a0, a1, a2, a3, b0, b1);
+                if (first) mma_first<F16>(pt, A[0], A[1], A[2], A[3], b0, b1);
+                else if constexpr (F16) lk_mma_f16_16816(pt, A[0], A[1], A[2], A[3], b0, b1);
+                else lk_mma_bf16_16816(pt, A[0], A[1], A[2], A[3], b0, b1);
                 if (last) {
                   acc[a][t][0] = fmaf(s0, pt[0], acc[a][t][0]);
                   acc[a][t][1] = fmaf(s0, pt[1], acc[a][t][1]);
@@ -394,6 +408,7 @@ cudaError_t launch_w4_linear(const W4Launch& a, cudaStream_t stream) {
   p.n_out = a.n_out;
   p.k_in = a.k_in;
   p.steps = steps_of(a.k_in);
+  p.full_steps = a.k_in / kStep;
   p.m = a.m;
   p.x_stride = a.x_stride;
   p.y_dtype = a.y_dtype;
