@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 32;  // moves per CTA
+constexpr int kMoveRows = 64;  // moves a CTA takes at a time
+constexpr int kAhead = 8;      // moves a thread has in flight
 
 struct EvictParams {
   uint8_t* k;
@@ -45,7 +46,7 @@ struct EvictParams {
   int32_t* dst;     // [units][cap]
   uint32_t* keys;   // [units][n_keys] where they do not fit in shared memory, else null
   int n_pages, page_shift, n_kv, row_bytes, is_i8, batch, width;
-  int max_len, budget, window, n_sink, cap, n_keys, in_place;
+  int max_len, budget, window, n_sink, cap, n_keys, in_place, lanes;
 };
 
 // Larger mass, larger key; +0 and -0 alike.
@@ -79,6 +80,23 @@ LK_DEVICE int block_scan(int x, int* warp_sums, int& sum) {
   return base + inc - x;
 }
 
+// Sum of the values of the warps before this one; the sum of all in `sum`.
+template <int WARPS>
+LK_DEVICE int warp_prefix(int x, int* warp_sums, int* sum = nullptr) {
+  __syncthreads();  // warp_sums of an earlier use are read
+  if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = x;
+  __syncthreads();
+  int base = 0, tot = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const int v = warp_sums[w];
+    if (w < (int)(threadIdx.x >> 5)) base += v;
+    tot += v;
+  }
+  if (sum) *sum = tot;
+  return base;
+}
+
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t smem_keys[];
@@ -92,7 +110,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
   const int n = max(0, min(__ldcg(p.seq_len + b), p.max_len));
   const int32_t* trow = p.table + (int64_t)b * p.width;
   auto row_of = [&](int t) {
-    return lk_paged_row(__ldcg(trow + (t >> p.page_shift)), t, h, p.n_pages, p.n_kv, p.page_shift);
+    return lk_paged_row(trow[t >> p.page_shift], t, h, p.n_pages, p.n_kv, p.page_shift);
   };
   if (n <= p.budget) {  // nothing leaves
     if (tid == 0) p.counts[unit] = 0;
@@ -108,28 +126,47 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
   uint32_t* keys = p.keys ? p.keys + (int64_t)unit * p.n_keys : smem_keys;
   const int newest = __ldcg(p.next_pos + b) - p.window;
 
-  // ---- keys; a protected token's top bit pattern is set once their number is known
+  // ---- keys, kBatch tokens' look-ups at a time; which are protected stays in `safe` (bit i: this thread's
+  // i-th token) for the first 64 a thread, and is read again for those behind
+  constexpr int kBatch = THREADS == 1024 ? 16 : 8;
+  auto is_safe = [&](int ps) { return ps < p.n_sink || ps >= newest; };
+  uint64_t safe = 0;
   int prot = 0;
-  for (int t = tid; t < n; t += THREADS) {
-    const int row = row_of(t);
-    uint32_t key = 1u;
-    if (row >= 0) {
-      key = mass_key(__ldcg(p.mass + row));
-      const int ps = __ldcg(p.pos + row);
-      prot += ps < p.n_sink || ps >= newest;
+  for (int i0 = 0; i0 * THREADS + tid < n; i0 += kBatch) {
+    int row[kBatch], ps[kBatch];
+    float m[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = (i0 + i) * THREADS + tid;
+      row[i] = t < n ? row_of(t) : -1;
     }
-    keys[t] = key;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      m[i] = row[i] >= 0 ? __ldcg(p.mass + row[i]) : NAN;
+      ps[i] = row[i] >= 0 ? __ldcg(p.pos + row[i]) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = (i0 + i) * THREADS + tid;
+      if (t < n) keys[t] = mass_key(m[i]);
+      if (row[i] >= 0 && is_safe(ps[i])) {
+        ++prot;
+        if (i0 + i < 64) safe |= 1ull << (i0 + i);
+      }
+    }
   }
   int n_prot;
   block_scan<THREADS>(prot, warp_sums, n_prot);
   const bool among = n_prot >= p.budget;  // select among the protected alone
   if (n_prot > 0) {
-    for (int t = tid; t < n; t += THREADS) {
-      const int row = row_of(t);
-      const int ps = row >= 0 ? __ldcg(p.pos + row) : 0;
-      const bool safe = row >= 0 && (ps < p.n_sink || ps >= newest);
-      if (safe && !among) keys[t] = 0xFFFFFFFFu;
-      if (!safe && among) keys[t] = 0u;
+    for (int i = 0, t = tid; t < n; ++i, t += THREADS) {
+      bool s = i < 64 && (safe >> i & 1);
+      if (i >= 64) {
+        const int row = row_of(t);
+        s = row >= 0 && is_safe(__ldcg(p.pos + row));
+      }
+      if (s && !among) keys[t] = 0xFFFFFFFFu;
+      if (!s && among) keys[t] = 0u;
     }
   }
 
@@ -170,48 +207,104 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     __syncthreads();  // hist and pick are read
   }
 
-  // ---- consecutive slots per thread (an odd number: distinct banks)
-  const int per = ((n + THREADS - 1) / THREADS) | 1;
-  const int t0 = min(n, tid * per), t1 = min(n, t0 + per);
+  // ---- consecutive slots per warp, 32 at a time; each key makes room for a flag: 1 = kept
+  const int lane = tid & 31, warp = tid >> 5;
+  const uint32_t below = (1u << lane) - 1;
+  constexpr int kWarps = THREADS / 32;
+  const int seg = ((n + THREADS - 1) / THREADS) * 32;
+  const int t0 = warp * seg, t1 = min(n, t0 + seg);
   int eq = 0;
-  for (int t = t0; t < t1; ++t) eq += keys[t] == lo;
-  int dummy;
-  const int eq0 = block_scan<THREADS>(eq, warp_sums, dummy);
-  int seen = eq0, holes = 0, movers = 0;
-  for (int t = t0; t < t1; ++t) {
-    const uint32_t key = keys[t];
-    bool kept = key > lo;
-    if (key == lo) kept = seen++ < need;
-    holes += t < p.budget && !kept;
-    movers += t >= p.budget && kept;
+#pragma unroll 4
+  for (int t = t0 + lane; t - lane < t1; t += 32) eq += __popc(__ballot_sync(0xffffffffu, t < t1 && keys[t] == lo));
+  int seen = warp_prefix<kWarps>(eq, warp_sums), holes = 0, movers = 0;
+#pragma unroll 4
+  for (int t = t0 + lane; t - lane < t1; t += 32) {
+    const uint32_t key = t < t1 ? keys[t] : 0u;
+    const uint32_t e = __ballot_sync(0xffffffffu, t < t1 && key == lo);
+    const bool kept = t < t1 && (key > lo || (key == lo && seen + __popc(e & below) < need));
+    seen += __popc(e);
+    if (t < t1) keys[t] = kept;
+    holes += __popc(__ballot_sync(0xffffffffu, t < t1 && t < p.budget && !kept));
+    movers += __popc(__ballot_sync(0xffffffffu, t >= p.budget && kept));
   }
-  int n_holes, n_movers;
-  int hole = block_scan<THREADS>(holes, warp_sums, n_holes);
-  int mover = block_scan<THREADS>(movers, warp_sums, n_movers);
+  int n_holes;
+  int hole = warp_prefix<kWarps>(holes, warp_sums, &n_holes);
+  int mover = warp_prefix<kWarps>(movers, warp_sums);
   int32_t* src = p.src + (int64_t)unit * p.cap;
   int32_t* dst = p.dst + (int64_t)unit * p.cap;
-  seen = eq0;
-  for (int t = t0; t < t1; ++t) {
-    const uint32_t key = keys[t];
-    bool kept = key > lo;
-    if (key == lo) kept = seen++ < need;
-    if (t < p.budget && !kept) dst[hole++] = row_of(t);
-    else if (t >= p.budget && kept) src[mover++] = row_of(t);
-    else if (t < p.budget && !p.in_place) {
-      const int row = row_of(t);
-      if (row >= 0) {
-        p.mass_out[row] = __ldcg(p.mass + row);
-        p.pos_out[row] = __ldcg(p.pos + row);
+#pragma unroll 4
+  for (int t = t0 + lane; t - lane < t1; t += 32) {
+    const bool kept = t < t1 && keys[t];
+    const uint32_t hb = __ballot_sync(0xffffffffu, t < t1 && t < p.budget && !kept);
+    const uint32_t mb = __ballot_sync(0xffffffffu, t >= p.budget && kept);
+    if (hb >> lane & 1) dst[hole + __popc(hb & below)] = t;
+    if (mb >> lane & 1) src[mover + __popc(mb & below)] = t;
+    hole += __popc(hb);
+    mover += __popc(mb);
+  }
+  __syncthreads();  // the lists (of slots so far) and flags are written
+  if (tid == 0) p.counts[unit] = n_holes;
+  if (!p.in_place) {
+    for (int i0 = 0; i0 * THREADS + tid < p.budget; i0 += kBatch) {
+      int row[kBatch], ps[kBatch];
+      float m[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int t = (i0 + i) * THREADS + tid;
+        row[i] = t < p.budget && keys[t] ? row_of(t) : -1;
       }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (row[i] >= 0) {
+          m[i] = __ldcg(p.mass + row[i]);
+          ps[i] = __ldcg(p.pos + row[i]);
+        }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (row[i] >= 0) {
+          p.mass_out[row[i]] = m[i];
+          p.pos_out[row[i]] = ps[i];
+        }
     }
   }
-  __syncthreads();  // the lists are written
-  if (tid == 0) p.counts[unit] = n_holes;
-  for (int i = tid; i < n_holes; i += THREADS) {
-    const int d = dst[i], s = src[i];
-    if (d < 0 || s < 0) continue;
-    p.mass_out[d] = __ldcg(p.mass + s);
-    p.pos_out[d] = __ldcg(p.pos + s);
+  // the moves: slots become rows, and their mass and positions go along
+  constexpr int kPairs = 4;
+  for (int i0 = 0; i0 * THREADS + tid < n_holes; i0 += kPairs) {
+    int d[kPairs], f[kPairs], ps[kPairs];
+    float m[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int j = (i0 + i) * THREADS + tid;
+      d[i] = j < n_holes ? dst[j] : -1;
+      f[i] = j < n_holes ? src[j] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+      if (d[i] >= 0) {
+        d[i] = row_of(d[i]);
+        f[i] = row_of(f[i]);
+        if (f[i] < 0) d[i] = -1;
+      } else {
+        d[i] = -2;  // behind the list
+      }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+      if (d[i] >= 0) {
+        m[i] = __ldcg(p.mass + f[i]);
+        ps[i] = __ldcg(p.pos + f[i]);
+      }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int j = (i0 + i) * THREADS + tid;
+      if (d[i] >= 0) {
+        p.mass_out[d[i]] = m[i];
+        p.pos_out[d[i]] = ps[i];
+      }
+      if (d[i] >= -1) {
+        dst[j] = d[i];
+        src[j] = f[i];
+      }
+    }
   }
 }
 
@@ -226,19 +319,36 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   const int count = __ldcg(p.counts + unit);
   const int32_t* src = p.src + (int64_t)unit * p.cap;
   const int32_t* dst = p.dst + (int64_t)unit * p.cap;
-  const int vec = p.row_bytes / 16;
-  const int64_t total = 2 * (int64_t)count * vec;
-  const int64_t step = (int64_t)gridDim.y * kMoveThreads;
-  for (int64_t i = (int64_t)blockIdx.y * kMoveThreads + threadIdx.x; i < total; i += step) {
-    const int r = (int)(i / vec), c = (int)(i - (int64_t)r * vec), m = r >> 1;
-    const int s = __ldcg(src + m), d = __ldcg(dst + m);
-    if (s < 0 || d < 0) continue;
-    uint8_t* base = (r & 1) ? p.v : p.k;
-    reinterpret_cast<uint4*>(base + (int64_t)d * p.row_bytes)[c] =
-        __ldcg(reinterpret_cast<const uint4*>(base + (int64_t)s * p.row_bytes) + c);
-    if (p.is_i8 && c == 0) {
-      float* sc = (r & 1) ? p.vs : p.ks;
-      sc[d] = __ldcg(sc + s);
+  // `lanes` lanes per move (the power of two above its 16-byte pieces, K's then V's; 32 take two turns)
+  const int vec = p.row_bytes / 16, pieces = 2 * vec;
+  const int sub = (int)threadIdx.x & (p.lanes - 1), per = kMoveThreads / p.lanes;
+  for (int m0 = blockIdx.y * kMoveRows; m0 < count; m0 += gridDim.y * kMoveRows) {
+    for (int m1 = m0 + (int)threadIdx.x / p.lanes; m1 < min(m0 + kMoveRows, count); m1 += kAhead * per) {
+      int s[kAhead], d[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const int m = m1 + e * per;
+        const bool in = m < min(m0 + kMoveRows, count);
+        s[e] = in ? __ldcg(src + m) : -1;
+        d[e] = in ? __ldcg(dst + m) : -1;
+      }
+      for (int c = sub; c < pieces; c += p.lanes) {
+        uint8_t* base = c < vec ? p.k : p.v;
+        const int off = 16 * (c < vec ? c : c - vec);
+        uint4 x[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          if (s[e] >= 0 && d[e] >= 0) x[e] = __ldcg(reinterpret_cast<const uint4*>(base + (int64_t)s[e] * p.row_bytes + off));
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          if (s[e] >= 0 && d[e] >= 0) *reinterpret_cast<uint4*>(base + (int64_t)d[e] * p.row_bytes + off) = x[e];
+        if (p.is_i8 && off == 0) {
+          float* sc = c < vec ? p.ks : p.vs;
+#pragma unroll
+          for (int e = 0; e < kAhead; ++e)
+            if (s[e] >= 0 && d[e] >= 0) sc[d[e]] = __ldcg(sc + s[e]);
+        }
+      }
     }
   }
 }
@@ -247,7 +357,7 @@ size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Keys a CTA holds in shared memory; longer sequences keep theirs in the workspace.
 constexpr int kSmemKeys = 48 * 1024;
-constexpr int kSmallKeys = 4096;  // up to here 256 threads a CTA
+constexpr int kSmallKeys = 4096;  // up to here 512 threads a CTA
 
 int move_cap(int max_len, int budget) { return std::max(0, std::min(budget, max_len - budget)); }
 
@@ -285,6 +395,8 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   p.n_kv = c.n_kv_heads;
   p.is_i8 = c.dtype == LK_I8;
   p.row_bytes = c.head_dim * (p.is_i8 ? 1 : 2);
+  p.lanes = 2;
+  while (p.lanes < 32 && p.lanes < p.row_bytes / 8) p.lanes *= 2;
   p.batch = c.batch;
   p.width = c.table_width;
   p.max_len = a.max_len;
@@ -303,7 +415,7 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   const size_t smem = spill || a.max_len <= a.budget ? 0 : (size_t)a.max_len * 4;
   cudaError_t e;
   if (a.max_len <= kSmallKeys) {
-    e = launch_pdl(select_kernel<256>, dim3(units), dim3(256), stream, p, smem);
+    e = launch_pdl(select_kernel<512>, dim3(units), dim3(512), stream, p, smem);
   } else {
     if (smem > 36 * 1024) {
       e = cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys * 4);

@@ -24,7 +24,7 @@
 //
 // One CTA an SM where that is one wave: tn tiles of 16 outputs by kn parts of
 // K, a warp each.  A warp's steps stream through its own ring in shared memory
-// (cp.async, no barrier), and with them its part of up to 8 rows of x; more
+// (cp.async, no barrier), and with them its part of a single row of x; more
 // rows are staged once for the tn warps of a part of K, which one named
 // barrier a step keeps together.  The parts' sums meet in shared memory.
 #include <atomic>
@@ -54,9 +54,9 @@ __host__ __device__ constexpr int record_bytes(int group, int mats) { return mat
 template <int GROUP, int R, int MATS>
 struct W4Shape {
   static constexpr int kMT = R <= 8 ? 1 : R / 8;   // products side by side
-  static constexpr bool kShared = R > 8;           // x is staged for several warps
+  static constexpr bool kShared = R > 1;           // x is staged for several warps
   static constexpr int kRec = record_bytes(GROUP, MATS);
-  static constexpr int kStages = R == 1 ? (MATS == 2 ? 4 : 6) : 3;
+  static constexpr int kStages = R <= 8 ? (MATS == 2 ? 4 : (R == 1 ? 6 : 5)) : 3;
   static constexpr int kXStage = R * kXStride;
   static constexpr int kStage = kRec + (kShared ? 0 : kXStage);  // a warp's own
   static constexpr int kRedRow = 17;
