@@ -11,10 +11,14 @@
 // protected tokens 0xFFFFFFFF, or, when they alone exceed the budget, all
 // others 0).  The budget-th largest key is found by narrowing an interval of
 // keys: 2048 bins over the current interval, then the bin that holds it, so
-// three passes (32 bits = 11 + 11 + 10).  Ties at that key go to the lowest slots: each thread owns
-// consecutive slots, so block-wide prefix sums over the threads give every
-// equal key, every hole and every moving token its number.  The CTA also
-// writes the kept mass and positions.
+// three passes (32 bits = 11 + 11 + 10).  Ties at that key go to the lowest
+// slots: each warp owns consecutive slots, so ballots and prefix sums over the
+// warps give every equal key, every hole and every moving token its number.
+// The CTA also writes the kept mass and positions.  Bound by instructions and
+// latency: hence four tokens an access and no look at ties where there are
+// none.  A cluster of 8 CTAs a unit with the bins summed over distributed
+// shared memory took 98 us for 16384 tokens a unit against 36 us (every CTA
+// reads every other's bins three times).
 // move_kernel: the listed rows of K and V (and int8 scales), 16 bytes a lane,
 // and the new lengths (which select_kernel's CTAs still read).
 // The holes lie below the budget and the moving rows at or above it, so the
@@ -25,8 +29,8 @@ namespace {
 
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 64;  // moves a CTA takes at a time
-constexpr int kAhead = 8;      // moves a thread has in flight
+constexpr int kMoveRows = 32;  // moves a CTA takes at a time
+constexpr int kAhead = 4;      // moves a thread has in flight
 
 struct EvictParams {
   uint8_t* k;
@@ -46,7 +50,7 @@ struct EvictParams {
   int32_t* dst;     // [units][cap]
   uint32_t* keys;   // [units][n_keys] where they do not fit in shared memory, else null
   int n_pages, page_shift, n_kv, row_bytes, is_i8, batch, width;
-  int max_len, budget, window, n_sink, cap, n_keys, in_place, lanes;
+  int max_len, budget, window, n_sink, cap, n_keys, seg_max, in_place, lanes;
 };
 
 // Larger mass, larger key; +0 and -0 alike.
@@ -56,254 +60,265 @@ LK_DEVICE uint32_t mass_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum over the block (every thread); total in `sum`.
-template <int THREADS>
-LK_DEVICE int block_scan(int x, int* warp_sums, int& sum) {
+// Exclusive prefix of one value a warp over the block's warps, and the sum of all.  `slots` is used once.
+template <int WARPS>
+LK_DEVICE int warp_prefix(int x, int* slots, int& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) slots[warp] = x;
+  __syncthreads();
+  const int v = lane < WARPS ? slots[lane] : 0;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < WARPS; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  all = __shfl_sync(0xffffffffu, inc, WARPS - 1);
+  return __shfl_sync(0xffffffffu, inc - v, warp);
+}
+
+// Exclusive prefix of one value a thread over the block.
+template <int WARPS>
+LK_DEVICE int block_scan(int x, int* slots) {
+  const int lane = threadIdx.x & 31;
   int inc = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  __syncthreads();  // warp_sums of an earlier scan are read
-  if (lane == 31) warp_sums[warp] = inc;
-  __syncthreads();
-  int base = 0, tot = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const int s = warp_sums[w];
-    if (w < warp) base += s;
-    tot += s;
-  }
-  sum = tot;
-  return base + inc - x;
+  int all;
+  return warp_prefix<WARPS>(__shfl_sync(0xffffffffu, inc, 31), slots, all) + inc - x;
 }
 
-// Sum of the values of the warps before this one; the sum of all in `sum`.
-template <int WARPS>
-LK_DEVICE int warp_prefix(int x, int* warp_sums, int* sum = nullptr) {
-  __syncthreads();  // warp_sums of an earlier use are read
-  if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = x;
-  __syncthreads();
-  int base = 0, tot = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    const int v = warp_sums[w];
-    if (w < (int)(threadIdx.x >> 5)) base += v;
-    tot += v;
-  }
-  if (sum) *sum = tot;
-  return base;
-}
-
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t smem_keys[];
-  __shared__ int hist[kBins];
-  __shared__ int warp_sums[THREADS / 32];
-  __shared__ int pick[2];
-  const int unit = blockIdx.x, b = unit / p.n_kv, h = unit - b * p.n_kv;
-  const int tid = threadIdx.x;
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ __align__(16) uint32_t smem_keys[];  // keys, then a bit a slot: kept
+  __shared__ __align__(16) int hist[3][kBins];
+  __shared__ int slots[7][kWarps];
+  __shared__ int pick[3][3];
+  const int unit = blockIdx.x;
+  const int b = unit / p.n_kv, h = unit - b * p.n_kv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   lk_grid_dep_wait();
   lk_grid_dep_launch();
   const int n = max(0, min(__ldcg(p.seq_len + b), p.max_len));
+  const int newest = __ldcg(p.next_pos + b) - p.window;
   const int32_t* trow = p.table + (int64_t)b * p.width;
-  auto row_of = [&](int t) {
-    return lk_paged_row(trow[t >> p.page_shift], t, h, p.n_pages, p.n_kv, p.page_shift);
+  const bool quads = p.page_shift >= 2;  // four slots from a multiple of four lie in one page
+  auto row_of = [&](int t) { return lk_paged_row(trow[t >> p.page_shift], t, h, p.n_pages, p.n_kv, p.page_shift); };
+  // rows (-1: none), mass and positions of the slots t .. t + 3 below `end`
+  auto load4 = [&](int t, int end, int (&row)[4], float (&m)[4], int (&ps)[4]) {
+    if (quads) {
+      const int r = t < end ? row_of(t) : -1;
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      int4 i = make_int4(0, 0, 0, 0);
+      if (r >= 0) {
+        f = __ldcg(reinterpret_cast<const float4*>(p.mass + r));
+        i = __ldcg(reinterpret_cast<const int4*>(p.pos + r));
+      }
+      m[0] = f.x; m[1] = f.y; m[2] = f.z; m[3] = f.w;
+      ps[0] = i.x; ps[1] = i.y; ps[2] = i.z; ps[3] = i.w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) row[e] = r >= 0 && t + e < end ? r + e : -1;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        row[e] = t + e < end ? row_of(t + e) : -1;
+        m[e] = row[e] >= 0 ? __ldcg(p.mass + row[e]) : 0.0f;
+        ps[e] = row[e] >= 0 ? __ldcg(p.pos + row[e]) : 0;
+      }
+    }
   };
+  auto is_safe = [&](int ps) { return ps < p.n_sink || ps >= newest; };
+
   if (n <= p.budget) {  // nothing leaves
     if (tid == 0) p.counts[unit] = 0;
     if (!p.in_place)
-      for (int t = tid; t < n; t += THREADS) {
-        const int row = row_of(t);
-        if (row < 0) continue;
-        p.mass_out[row] = __ldcg(p.mass + row);
-        p.pos_out[row] = __ldcg(p.pos + row);
+      for (int t = 4 * tid; t < n; t += 4 * kThreads) {
+        int row[4], ps[4];
+        float m[4];
+        load4(t, n, row, m, ps);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row[e] >= 0) {
+            p.mass_out[row[e]] = m[e];
+            p.pos_out[row[e]] = ps[e];
+          }
       }
     return;
   }
   uint32_t* keys = p.keys ? p.keys + (int64_t)unit * p.n_keys : smem_keys;
-  const int newest = __ldcg(p.next_pos + b) - p.window;
+  uint32_t* kept = keys + p.seg_max;
 
-  // ---- keys, kBatch tokens' look-ups at a time; which are protected stays in `safe` (bit i: this thread's
-  // i-th token) for the first 64 a thread, and is read again for those behind
-  constexpr int kBatch = THREADS == 1024 ? 16 : 8;
-  auto is_safe = [&](int ps) { return ps < p.n_sink || ps >= newest; };
+  // ---- keys; which tokens are protected stays in `safe` (four bits a turn) for 16 turns, and is read again behind
+  for (int i = tid; i < 3 * kBins / 4; i += kThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
   uint64_t safe = 0;
   int prot = 0;
-  for (int i0 = 0; i0 * THREADS + tid < n; i0 += kBatch) {
-    int row[kBatch], ps[kBatch];
-    float m[kBatch];
+#pragma unroll 2
+  for (int i = 0; 4 * (i * kThreads + tid) < n; ++i) {
+    const int t = 4 * (i * kThreads + tid);
+    int row[4], ps[4];
+    float m[4];
+    load4(t, n, row, m, ps);
+    uint32_t key[4], bits = 0;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int t = (i0 + i) * THREADS + tid;
-      row[i] = t < n ? row_of(t) : -1;
+    for (int e = 0; e < 4; ++e) {
+      key[e] = row[e] >= 0 ? mass_key(m[e]) : 1u;
+      bits |= (uint32_t)(row[e] >= 0 && is_safe(ps[e])) << e;
     }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      m[i] = row[i] >= 0 ? __ldcg(p.mass + row[i]) : NAN;
-      ps[i] = row[i] >= 0 ? __ldcg(p.pos + row[i]) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int t = (i0 + i) * THREADS + tid;
-      if (t < n) keys[t] = mass_key(m[i]);
-      if (row[i] >= 0 && is_safe(ps[i])) {
-        ++prot;
-        if (i0 + i < 64) safe |= 1ull << (i0 + i);
-      }
-    }
+    *reinterpret_cast<uint4*>(keys + t) = make_uint4(key[0], key[1], key[2], key[3]);
+    prot += __popc(bits);
+    if (i < 16) safe |= (uint64_t)bits << (4 * i);
   }
   int n_prot;
-  block_scan<THREADS>(prot, warp_sums, n_prot);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) prot += __shfl_xor_sync(0xffffffffu, prot, o);
+  warp_prefix<kWarps>(prot, slots[0], n_prot);
   const bool among = n_prot >= p.budget;  // select among the protected alone
   if (n_prot > 0) {
-    for (int i = 0, t = tid; t < n; ++i, t += THREADS) {
-      bool s = i < 64 && (safe >> i & 1);
-      if (i >= 64) {
-        const int row = row_of(t);
-        s = row >= 0 && is_safe(__ldcg(p.pos + row));
+    for (int i = 0; 4 * (i * kThreads + tid) < n; ++i) {
+      const int t = 4 * (i * kThreads + tid);
+      uint32_t bits = i < 16 ? (uint32_t)(safe >> (4 * i)) & 15u : 0;
+      if (i >= 16) {
+        int row[4], ps[4];
+        float m[4];
+        load4(t, n, row, m, ps);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bits |= (uint32_t)(row[e] >= 0 && is_safe(ps[e])) << e;
       }
-      if (s && !among) keys[t] = 0xFFFFFFFFu;
-      if (!s && among) keys[t] = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((bits >> e & 1) && !among) keys[t + e] = 0xFFFFFFFFu;
+        if (!(bits >> e & 1) && among) keys[t + e] = 0u;
+      }
     }
   }
 
-  // ---- the budget-th largest key: `need` of the keys in [lo, lo + 2^bits) are still wanted
+  // ---- the budget-th largest key: `need` of the keys in [lo, lo + 2^bits) are still wanted, `equal` there are
   uint32_t lo = 0;
-  int bits = 32, need = p.budget;
-  while (bits > 0) {
-    const int shift = max(0, bits - 11);
-    for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
-    __syncthreads();
-    for (int t = tid; t < n; t += THREADS) {
-      const uint32_t d = keys[t] - lo;
-      if (keys[t] >= lo && (bits == 32 || d < (1u << bits))) atomicAdd(&hist[d >> shift], 1);
+  int bits = 32, need = p.budget, equal = 0;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+#pragma unroll 2
+    for (int t = 4 * tid; t < n; t += 4 * kThreads) {
+      const uint4 k4 = *reinterpret_cast<const uint4*>(keys + t);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t d = k[e] - lo;  // keys below lo wrap around to at least 2^bits
+        if (t + e < n && (pass == 0 || (d >> bits) == 0)) atomicAdd(&hist[pass][d >> shift], 1);
+      }
     }
     __syncthreads();
-    // bins from the top: thread i owns bins [kPer i', ...) with i' counted from the top
-    constexpr int kPer = kBins / THREADS;
+    // consecutive bins a thread, from the top
+    constexpr int kPer = kBins / kThreads;
+    const int top = kBins - kPer * (tid + 1);
+    int bin[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) bin[e] = hist[pass][top + e];
     int mine = 0;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) mine += hist[kBins - 1 - (tid * kPer + e)];
-    int all;
-    int above = block_scan<THREADS>(mine, warp_sums, all);
+    for (int e = 0; e < kPer; ++e) mine += bin[e];
+    int above = block_scan<kWarps>(mine, slots[1 + pass]);
     if (above < need && above + mine >= need) {
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int bin = kBins - 1 - (tid * kPer + e), x = hist[bin];
-        if (above < need && above + x >= need) {
-          pick[0] = bin;
-          pick[1] = above;
+      for (int e = kPer - 1; e >= 0; --e) {
+        if (above < need && above + bin[e] >= need) {
+          pick[pass][0] = top + e;
+          pick[pass][1] = above;
+          pick[pass][2] = bin[e];
         }
-        above += x;
+        above += bin[e];
       }
     }
     __syncthreads();
-    lo += (uint32_t)pick[0] << shift;
-    need -= pick[1];
+    lo += (uint32_t)pick[pass][0] << shift;
+    need -= pick[pass][1];
+    equal = pick[pass][2];
     bits = shift;
-    __syncthreads();  // hist and pick are read
   }
 
-  // ---- consecutive slots per warp, 32 at a time; each key makes room for a flag: 1 = kept
-  const int lane = tid & 31, warp = tid >> 5;
+  // ---- consecutive slots per warp, 32 at a time
   const uint32_t below = (1u << lane) - 1;
-  constexpr int kWarps = THREADS / 32;
-  const int seg = ((n + THREADS - 1) / THREADS) * 32;
-  const int t0 = warp * seg, t1 = min(n, t0 + seg);
-  int eq = 0;
-#pragma unroll 4
-  for (int t = t0 + lane; t - lane < t1; t += 32) eq += __popc(__ballot_sync(0xffffffffu, t < t1 && keys[t] == lo));
-  int seen = warp_prefix<kWarps>(eq, warp_sums), holes = 0, movers = 0;
-#pragma unroll 4
-  for (int t = t0 + lane; t - lane < t1; t += 32) {
-    const uint32_t key = t < t1 ? keys[t] : 0u;
-    const uint32_t e = __ballot_sync(0xffffffffu, t < t1 && key == lo);
-    const bool kept = t < t1 && (key > lo || (key == lo && seen + __popc(e & below) < need));
-    seen += __popc(e);
-    if (t < t1) keys[t] = kept;
-    holes += __popc(__ballot_sync(0xffffffffu, t < t1 && t < p.budget && !kept));
-    movers += __popc(__ballot_sync(0xffffffffu, t >= p.budget && kept));
+  const int words = (n + 31) / 32, per = (words + kWarps - 1) / kWarps;
+  const int w0 = min(words, warp * per), w1 = min(words, w0 + per);
+  const bool ties = need < equal;
+  int seen = 0, holes = 0, movers = 0, all;
+  if (ties) {
+    int eq = 0;
+    for (int w = w0; w < w1; ++w) {
+      const int t = 32 * w + lane;
+      eq += __popc(__ballot_sync(0xffffffffu, t < n && keys[t] == lo));
+    }
+    seen = warp_prefix<kWarps>(eq, slots[4], all);
+  }
+  for (int w = w0; w < w1; ++w) {
+    const int t = 32 * w + lane;
+    const uint32_t key = t < n ? keys[t] : 0u;
+    bool keep = t < n && key >= lo;
+    if (ties) {
+      const uint32_t e = __ballot_sync(0xffffffffu, t < n && key == lo);
+      if (key == lo) keep = keep && seen + __popc(e & below) < need;
+      seen += __popc(e);
+    }
+    const uint32_t k = __ballot_sync(0xffffffffu, keep);
+    const int in_budget = min(32, max(0, p.budget - 32 * w));  // slots of the word below the budget
+    const uint32_t low = in_budget == 32 ? 0xffffffffu : (1u << in_budget) - 1;
+    if (lane == 0) kept[w] = k;
+    holes += __popc(~k & low);  // the budget lies below n: such slots are all live
+    movers += __popc(k & ~low);
   }
   int n_holes;
-  int hole = warp_prefix<kWarps>(holes, warp_sums, &n_holes);
-  int mover = warp_prefix<kWarps>(movers, warp_sums);
+  int hole = warp_prefix<kWarps>(holes, slots[5], n_holes);
+  int mover = warp_prefix<kWarps>(movers, slots[6], all);
   int32_t* src = p.src + (int64_t)unit * p.cap;
   int32_t* dst = p.dst + (int64_t)unit * p.cap;
-#pragma unroll 4
-  for (int t = t0 + lane; t - lane < t1; t += 32) {
-    const bool kept = t < t1 && keys[t];
-    const uint32_t hb = __ballot_sync(0xffffffffu, t < t1 && t < p.budget && !kept);
-    const uint32_t mb = __ballot_sync(0xffffffffu, t >= p.budget && kept);
+  for (int w = w0; w < w1; ++w) {
+    const uint32_t k = kept[w];
+    const int t = 32 * w + lane;
+    const int in_budget = min(32, max(0, p.budget - 32 * w));
+    const uint32_t low = in_budget == 32 ? 0xffffffffu : (1u << in_budget) - 1;
+    const uint32_t hb = ~k & low, mb = k & ~low;
     if (hb >> lane & 1) dst[hole + __popc(hb & below)] = t;
     if (mb >> lane & 1) src[mover + __popc(mb & below)] = t;
     hole += __popc(hb);
     mover += __popc(mb);
   }
-  __syncthreads();  // the lists (of slots so far) and flags are written
   if (tid == 0) p.counts[unit] = n_holes;
+  __syncthreads();  // the lists and `kept` are written
   if (!p.in_place) {
-    for (int i0 = 0; i0 * THREADS + tid < p.budget; i0 += kBatch) {
-      int row[kBatch], ps[kBatch];
-      float m[kBatch];
+#pragma unroll 2
+    for (int t = 4 * tid; t < p.budget; t += 4 * kThreads) {
+      const uint32_t k = kept[t >> 5] >> (t & 31) & 15u;
+      int row[4], ps[4];
+      float m[4];
+      load4(t, p.budget, row, m, ps);
+      if (quads && k == 15u && row[0] >= 0 && row[3] >= 0) {
+        *reinterpret_cast<float4*>(p.mass_out + row[0]) = make_float4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<int4*>(p.pos_out + row[0]) = make_int4(ps[0], ps[1], ps[2], ps[3]);
+      } else {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int t = (i0 + i) * THREADS + tid;
-        row[i] = t < p.budget && keys[t] ? row_of(t) : -1;
+        for (int e = 0; e < 4; ++e)
+          if ((k >> e & 1) && row[e] >= 0) {
+            p.mass_out[row[e]] = m[e];
+            p.pos_out[row[e]] = ps[e];
+          }
       }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (row[i] >= 0) {
-          m[i] = __ldcg(p.mass + row[i]);
-          ps[i] = __ldcg(p.pos + row[i]);
-        }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (row[i] >= 0) {
-          p.mass_out[row[i]] = m[i];
-          p.pos_out[row[i]] = ps[i];
-        }
     }
   }
-  // the moves: slots become rows, and their mass and positions go along
-  constexpr int kPairs = 4;
-  for (int i0 = 0; i0 * THREADS + tid < n_holes; i0 += kPairs) {
-    int d[kPairs], f[kPairs], ps[kPairs];
-    float m[kPairs];
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const int j = (i0 + i) * THREADS + tid;
-      d[i] = j < n_holes ? dst[j] : -1;
-      f[i] = j < n_holes ? src[j] : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-      if (d[i] >= 0) {
-        d[i] = row_of(d[i]);
-        f[i] = row_of(f[i]);
-        if (f[i] < 0) d[i] = -1;
-      } else {
-        d[i] = -2;  // behind the list
-      }
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-      if (d[i] >= 0) {
-        m[i] = __ldcg(p.mass + f[i]);
-        ps[i] = __ldcg(p.pos + f[i]);
-      }
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const int j = (i0 + i) * THREADS + tid;
-      if (d[i] >= 0) {
-        p.mass_out[d[i]] = m[i];
-        p.pos_out[d[i]] = ps[i];
-      }
-      if (d[i] >= -1) {
-        dst[j] = d[i];
-        src[j] = f[i];
-      }
+  // ---- the moves: slots become rows, and their mass and positions go along
+  for (int j = tid; j < n_holes; j += kThreads) {
+    int d = row_of(__ldcg(dst + j));
+    const int f = row_of(__ldcg(src + j));
+    if (f < 0) d = -1;
+    dst[j] = d;
+    src[j] = f;
+    if (d >= 0) {
+      p.mass_out[d] = __ldcg(p.mass + f);
+      p.pos_out[d] = __ldcg(p.pos + f);
     }
   }
 }
@@ -355,11 +370,23 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Keys a CTA holds in shared memory; longer sequences keep theirs in the workspace.
-constexpr int kSmemKeys = 48 * 1024;
-constexpr int kSmallKeys = 4096;  // up to here 512 threads a CTA
+// Slots a CTA holds keys for in shared memory; longer sequences keep theirs in the workspace.
+constexpr int kSmemKeys = 40 * 1024;
+int seg_of(int max_len) { return (max_len + 127) & ~127; }
+size_t spill_words(int max_len) { return (size_t)seg_of(max_len) / 32 * 33; }  // keys and bits
+bool spills(int max_len, int budget) { return max_len > budget && seg_of(max_len) > kSmemKeys; }
 
 int move_cap(int max_len, int budget) { return std::max(0, std::min(budget, max_len - budget)); }
+
+template <int THREADS>
+cudaError_t launch_select(int units, size_t smem, const EvictParams& p, cudaStream_t stream) {
+  if (smem > 20 * 1024) {  // with the 25 KB of bins beyond the default limit
+    const cudaError_t e = cudaFuncSetAttribute(select_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSmemKeys / 32 * 33 * 4);
+    if (e != cudaSuccess) return e;
+  }
+  return lk::launch_pdl(select_kernel<THREADS>, dim3(units), dim3(THREADS), stream, p, smem);
+}
 
 }  // namespace
 
@@ -370,7 +397,7 @@ namespace lk {
 size_t paged_evict_workspace_bytes(int units, int max_len, int budget) {
   const size_t lists = round256((size_t)units * move_cap(max_len, budget) * 4);
   return round256((size_t)units * 4) + 2 * lists +
-         (max_len > budget && max_len > kSmemKeys ? (size_t)units * max_len * 4 : 0);
+         (spills(max_len, budget) ? (size_t)units * spill_words(max_len) * 4 : 0);
 }
 
 cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
@@ -409,20 +436,16 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   p.counts = reinterpret_cast<int32_t*>(ws);
   p.src = reinterpret_cast<int32_t*>(ws + round256((size_t)units * 4));
   p.dst = reinterpret_cast<int32_t*>(ws + round256((size_t)units * 4) + lists);
-  const bool spill = a.max_len > a.budget && a.max_len > kSmemKeys;
+  const bool spill = spills(a.max_len, a.budget);
   p.keys = spill ? reinterpret_cast<uint32_t*>(ws + round256((size_t)units * 4) + 2 * lists) : nullptr;
-  p.n_keys = a.max_len;
-  const size_t smem = spill || a.max_len <= a.budget ? 0 : (size_t)a.max_len * 4;
+  p.n_keys = (int)spill_words(a.max_len);
+  p.seg_max = seg_of(a.max_len);
+  const size_t smem = spill || a.max_len <= a.budget ? 0 : (size_t)p.seg_max / 32 * 33 * 4;
   cudaError_t e;
-  if (a.max_len <= kSmallKeys) {
-    e = launch_pdl(select_kernel<512>, dim3(units), dim3(512), stream, p, smem);
-  } else {
-    if (smem > 36 * 1024) {
-      e = cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys * 4);
-      if (e != cudaSuccess) return e;
-    }
-    e = launch_pdl(select_kernel<1024>, dim3(units), dim3(1024), stream, p, smem);
-  }
+  // threads for about four slots each
+  if (a.max_len <= 1024) e = launch_select<256>(units, smem, p, stream);
+  else if (a.max_len <= 4096) e = launch_select<512>(units, smem, p, stream);
+  else e = launch_select<1024>(units, smem, p, stream);
   if (e != cudaSuccess) return e;
   const int chunks = std::max(1, std::min(1024, (p.cap + kMoveRows - 1) / kMoveRows));
   return launch_pdl(move_kernel, dim3(units, chunks), dim3(kMoveThreads), stream, p);

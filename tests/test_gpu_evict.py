@@ -79,8 +79,9 @@ def test_evict_in_place(case, kind):
     compare(pages, cache, want, lens, budget)
 
 
-@pytest.mark.parametrize("lens,budget", [([70000], 30000), ([60000, 100], 50000)])
-def test_evict_longer_than_shared_memory(lens, budget):
+@pytest.mark.parametrize("lens,budget", [([70000], 30000), ([60000, 100], 50000), ([30001], 7), ([2000, 100001], 1999)])
+def test_evict_long_sequences(lens, budget):
+    # longer than shared memory holds keys for
     import rank_latent_kv_lk_b200 as lk
     B, page, dim = len(lens), 512, 16
     width = -(-max(lens) // page)
