@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 32;  // moves a CTA takes at a time
 constexpr int kAhead = 4;      // moves a thread has in flight
 
 struct EvictParams {
@@ -334,37 +333,48 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   const int count = __ldcg(p.counts + unit);
   const int32_t* src = p.src + (int64_t)unit * p.cap;
   const int32_t* dst = p.dst + (int64_t)unit * p.cap;
-  // `lanes` lanes per move (the power of two above its 16-byte pieces, K's then V's; 32 take two turns)
+  // `lanes` lanes per move (the power of two above its 16-byte pieces, K's then V's; 32 take turns)
   const int vec = p.row_bytes / 16, pieces = 2 * vec;
   const int sub = (int)threadIdx.x & (p.lanes - 1), per = kMoveThreads / p.lanes;
-  for (int m0 = blockIdx.y * kMoveRows; m0 < count; m0 += gridDim.y * kMoveRows) {
-    for (int m1 = m0 + (int)threadIdx.x / p.lanes; m1 < min(m0 + kMoveRows, count); m1 += kAhead * per) {
-      int s[kAhead], d[kAhead];
+  // kAhead moves a thread at a time; the next ones' rows are looked up while these travel
+  const int stride = gridDim.y * per * kAhead;
+  int s[kAhead], d[kAhead];
+  auto look_up = [&](int m0) {
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e) {
-        const int m = m1 + e * per;
-        const bool in = m < min(m0 + kMoveRows, count);
-        s[e] = in ? __ldcg(src + m) : -1;
-        d[e] = in ? __ldcg(dst + m) : -1;
-      }
-      for (int c = sub; c < pieces; c += p.lanes) {
-        uint8_t* base = c < vec ? p.k : p.v;
-        const int off = 16 * (c < vec ? c : c - vec);
-        uint4 x[kAhead];
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e)
-          if (s[e] >= 0 && d[e] >= 0) x[e] = __ldcg(reinterpret_cast<const uint4*>(base + (int64_t)s[e] * p.row_bytes + off));
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e)
-          if (s[e] >= 0 && d[e] >= 0) *reinterpret_cast<uint4*>(base + (int64_t)d[e] * p.row_bytes + off) = x[e];
-        if (p.is_i8 && off == 0) {
-          float* sc = c < vec ? p.ks : p.vs;
-#pragma unroll
-          for (int e = 0; e < kAhead; ++e)
-            if (s[e] >= 0 && d[e] >= 0) sc[d[e]] = __ldcg(sc + s[e]);
-        }
-      }
+    for (int e = 0; e < kAhead; ++e) {
+      const int m = m0 + e * per;
+      s[e] = m < count ? __ldcg(src + m) : -1;
+      d[e] = m < count ? __ldcg(dst + m) : -1;
     }
+  };
+  int m0 = blockIdx.y * per * kAhead + (int)threadIdx.x / p.lanes;
+  look_up(m0);
+  for (; m0 < count; m0 += stride) {
+    int64_t from[kAhead], to[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const bool in = s[e] >= 0 && d[e] >= 0;
+      from[e] = in ? (int64_t)s[e] * p.row_bytes : -1;
+      to[e] = (int64_t)d[e] * p.row_bytes;
+    }
+    for (int c = sub; c < pieces; c += p.lanes) {
+      uint8_t* base = (c < vec ? p.k : p.v) + 16 * (c < vec ? c : c - vec);
+      uint4 x[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (from[e] >= 0) x[e] = __ldcg(reinterpret_cast<const uint4*>(base + from[e]));
+      if (p.is_i8 && (c == 0 || c == vec)) {
+        float* sc = c < vec ? p.ks : p.vs;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          if (from[e] >= 0) sc[d[e]] = __ldcg(sc + s[e]);
+      }
+      if (c + p.lanes >= pieces) look_up(m0 + stride);
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (from[e] >= 0) *reinterpret_cast<uint4*>(base + to[e]) = x[e];
+    }
+    if (sub >= pieces) look_up(m0 + stride);
   }
 }
 
@@ -447,7 +457,10 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   else if (a.max_len <= 4096) e = launch_select<512>(units, smem, p, stream);
   else e = launch_select<1024>(units, smem, p, stream);
   if (e != cudaSuccess) return e;
-  const int chunks = std::max(1, std::min(1024, (p.cap + kMoveRows - 1) / kMoveRows));
+  // CTAs for a unit's most moves, but no more in all than twice what stays resident (dealing all units' moves
+  // out in equal ranges needs a prefix sum per CTA, which cost more than ragged batches gain)
+  const int rows = kMoveThreads / p.lanes * kAhead;
+  const int chunks = std::max(1, std::min((p.cap + rows - 1) / rows, 8 * a.num_sms / units));
   return launch_pdl(move_kernel, dim3(units, chunks), dim3(kMoveThreads), stream, p);
 }
 

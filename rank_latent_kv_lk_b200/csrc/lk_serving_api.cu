@@ -224,6 +224,7 @@ lk_status lk_paged_evict(const lk_paged_cache* cache, const int32_t* page_table,
   a.pos_out = pos_out;
   a.seq_len_out = seq_len_out;
   a.workspace = workspace;
+  a.num_sms = num_sms();
   cudaError_t e = lk::launch_paged_evict(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "lk_paged_evict");
   return LK_OK;

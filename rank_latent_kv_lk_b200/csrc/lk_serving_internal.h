@@ -84,6 +84,7 @@ struct PagedEvictLaunch {
   int32_t* pos_out;
   int32_t* seq_len_out;
   void* workspace;
+  int num_sms;
 };
 size_t paged_evict_workspace_bytes(int units, int max_len, int budget);
 cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream);
