@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
     __syncthreads();
 
     float o[S::kSteps][NT][4], m[NT][2], l[NT][2], sf[NT][2];
-    float vref = 0.0f;
+    float vref = 0.0f, vinv = 0.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -388,7 +388,9 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
     const int f_row = (lane & 7) + (lane & 8);  // ldmatrix: this lane's row and chunk of a pair
     const uint32_t f_at = f_row * S::kRowB;
     const uint32_t f_ch = ((lane >> 4) ^ swizzle<S::kCh>(f_row)) << 4;
-    for (; blk < s1; blk += kWarps) {
+    // the block's scores of heads 2 tig, tokens gid
+    float* sp = p.scores + (((int64_t)b_start * per_seq + (int64_t)hc * nb + blk) * p.hs + 2 * tig) * kTok + gid;
+    for (; blk < s1; blk += kWarps, sp += kWarps * p.hs * kTok) {
       // ---- request the block S::kStages - 1 ahead, then wait for this one
       {
         const int ahead = blk + (S::kStages - 1) * kWarps;
@@ -461,19 +463,16 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
           if (!((live >> (gid + 8)) & 1)) c[nt][2] = c[nt][3] = -INFINITY;
         }
         if (p.scores) {
-          const int64_t g = ((int64_t)b_start * per_seq + (int64_t)hc * nb + blk) * p.hs;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = 8 * nt + 2 * tig + e;
-            if (j < heads) {
-              float* dst = p.scores + (g + j) * kTok + gid;
-              dst[0] = c[nt][e];
-              dst[8] = c[nt][2 + e];
+          for (int e = 0; e < 2; ++e)
+            if (8 * nt + 2 * tig + e < heads) {
+              sp[(8 * nt + e) * kTok] = c[nt][e];
+              sp[(8 * nt + e) * kTok + 8] = c[nt][2 + e];
             }
-          }
         }
         moved |= fmaxf(c[nt][0], c[nt][2]) > m[nt][0] + kSlack || fmaxf(c[nt][1], c[nt][3]) > m[nt][1] + kSlack;
       }
+      if constexpr (DT == DT_I8) moved |= fmaxf(fabsf(vs0), fabsf(vs1)) > vref;
       float alpha[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) alpha[nt][0] = alpha[nt][1] = 1.0f;
@@ -506,20 +505,21 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
       }
       float grow = 1.0f;
       if constexpr (DT == DT_I8) {
-        // the largest V scale of the block, as the power of two above it
-        float a = fmaxf(fabsf(vs0), fabsf(vs1));
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
-        if (a > vref) {  // the same in every lane
-          const float up = __uint_as_float(min((__float_as_uint(a) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
-          grow = vref / up;
-          vref = up;
-          moved = true;
+        if (moved) {
+          // the largest V scale of the block, as the power of two above it
+          float a = fmaxf(fabsf(vs0), fabsf(vs1));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
+          if (a > vref) {  // the same in every lane
+            const float up = __uint_as_float(min((__float_as_uint(a) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
+            grow = vref / up;
+            vref = up;
+            vinv = 1.0f / up;
+          }
         }
-        const float inv = vref > 0.0f ? 1.0f / vref : 0.0f;
-        vs0 *= inv;
-        vs1 *= inv;
+        vs0 *= vinv;
+        vs1 *= vinv;
       }
       if (moved) {
 #pragma unroll
@@ -646,9 +646,9 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
 }
 
 // ---------------------------------------------------------------- joining the partials
-// CTAs [0, batch * n_heads): one (sequence, head) each: its pieces' weights,
-// then out = sum_c w_c O_c / sum_c w_c l_c, the pieces dealt out to groups of
-// D / 4 threads.  CTAs behind them (accumulate): kMassTok slots of one
+// CTAs [0, n_out): a warp per (sequence, head), or a whole CTA where a unit
+// has many pieces: their weights, then out = sum_c w_c O_c / sum_c w_c l_c.
+// CTAs behind them (accumulate): kMassTok slots of one
 // (sequence, kv head), four a thread: mass += sum over the heads of
 // exp2(s - M) / L.  Latency-bound: what does not depend on the statistics
 // (pieces, scores, page table, mass) is requested before they are reduced.
@@ -666,6 +666,7 @@ struct JoinParams {
   void* out;
   int grid;  // CTAs of the split kernel
   int n_pages, page_shift, n_kv, D, batch, width, group, nch, max_len, hp, hs, out_dtype, mass_chunks;
+  int n_out, wph;  // CTAs for the outputs, warps a head
   float offset;  // log2 of the factor the sums are held with
 };
 
@@ -708,28 +709,34 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   const int n_heads = p.n_kv * p.group;
   lk_grid_dep_wait();
   lk_grid_dep_launch();
-  const int n_out = p.batch * n_heads;
-  if ((int)blockIdx.x < n_out) {
-    const int b = blockIdx.x / n_heads, j = blockIdx.x - b * n_heads;
+  if ((int)blockIdx.x < p.n_out) {
+    // p.wph warps a head: lanes over float4 columns, the pieces dealt out to the warps (and, up to D = 64, to the
+    // halves of a warp or more)
+    const int per_cta = (kJoinThreads / 32) / p.wph;
+    const int head = blockIdx.x * per_cta + warp / p.wph;
     const int64_t N = (int64_t)__ldcg(p.starts + p.batch) * per_seq;
-    const int b0 = __ldcg(p.starts + b), nb = __ldcg(p.starts + b + 1) - b0;
+    const bool on = head < p.batch * n_heads;
+    const int b = on ? head / n_heads : 0, j = on ? head - b * n_heads : 0;
+    const int b0 = __ldcg(p.starts + b), nb = on ? __ldcg(p.starts + b + 1) - b0 : 0;
     const int h = j / p.group, jg = j - h * p.group;
     const int ch = jg / p.hp, jc = jg - ch * p.hp;
     const int hc = h * p.nch + ch, unit = b * per_seq + hc;
-    const int vec = p.D / 4;                 // float4 columns
-    const int groups = kJoinThreads / vec;   // D <= 256: at least 4
-    const int g = threadIdx.x / vec, d = threadIdx.x - g * vec;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float inv = 0.0f;
-    if (nb > 0) {
-      const Pieces pc = unit_pieces(p, (int64_t)b0 * per_seq + (int64_t)hc * nb, nb, N);
-      constexpr int kAhead = 4;
-      float4 x[kAhead];
-      float mc[kAhead];
+    const int vec = p.D / 4;                   // float4 columns, up to 64
+    const int threads = p.wph * 32, tid = (warp % p.wph) * 32 + lane;
+    const int groups = max(1, threads / vec);  // a single warp takes more than 32 columns in turns
+    const int g = threads < vec ? 0 : tid / vec;
+    float2 s = make_float2(-INFINITY, 0.0f);
+    Pieces pc{0, -1};
+    if (nb > 0) pc = unit_pieces(p, (int64_t)b0 * per_seq + (int64_t)hc * nb, nb, N);
+    constexpr int kAhead = 4;
+    float4 x[kAhead];
+    float mc[kAhead];
+    for (int d = threads < vec ? tid : tid - g * vec, turn = 0; turn == 0 || d < vec; d += threads, ++turn) {
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       auto load = [&](int c, float4& xv, float& mv) {
         xv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         mv = -INFINITY;
-        if (g < groups && c <= pc.c1) {
+        if (g < groups && d < vec && c <= pc.c1) {
           const int64_t at = ((int64_t)c + unit) * p.hp + jc;
           mv = __ldcg(p.stats + at * 2);
           xv = __ldcg(reinterpret_cast<const float4*>(p.part + at * p.D) + d);
@@ -737,9 +744,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
       };
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) load(pc.c0 + g + i * groups, x[i], mc[i]);
-      const float2 s = warp_stats(p, pc, unit, jc);
+      if (turn == 0) s = warp_stats(p, pc, unit, jc);  // while the pieces travel
       // every score -infinity (L = 0): zeros
-      inv = s.y == 0.0f ? 0.0f : 1.0f / s.y;
+      const float inv = s.y == 0.0f ? 0.0f : 1.0f / s.y;
       for (int c = pc.c0 + g; c <= pc.c1; c += kAhead * groups) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -751,40 +758,45 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
           load(c + (i + kAhead) * groups, x[i], mc[i]);
         }
       }
-    }
-    if (g < groups) red[g * vec + d] = acc;
-    __syncthreads();
-    if ((int)threadIdx.x < vec) {
-      for (int i = 1; i < groups; ++i) {
-        const float4 x = red[i * vec + d];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
+      if (groups > 1) {  // the same for every warp of the launch
+        float4* r = red + (warp / p.wph) * threads;
+        if (g < groups) r[g * vec + d] = acc;
+        __syncthreads();
+        if (g == 0)
+          for (int i = 1; i < groups; ++i) {
+            const float4 y = r[i * vec + d];
+            acc.x += y.x;
+            acc.y += y.y;
+            acc.z += y.z;
+            acc.w += y.w;
+          }
       }
-      acc.x *= inv;
-      acc.y *= inv;
-      acc.z *= inv;
-      acc.w *= inv;
-      const int64_t at = (int64_t)blockIdx.x * vec + d;
-      if (p.out_dtype == LK_F32) {
-        reinterpret_cast<float4*>(p.out)[at] = acc;
-      } else {
-        uint2 w;
-        if (p.out_dtype == LK_BF16) {
-          w.x = lk_pack_bf16x2(acc.x, acc.y);
-          w.y = lk_pack_bf16x2(acc.z, acc.w);
+      if (on && g == 0 && d < vec) {
+        acc.x *= inv;
+        acc.y *= inv;
+        acc.z *= inv;
+        acc.w *= inv;
+        const int64_t at = (int64_t)head * vec + d;
+        if (p.out_dtype == LK_F32) {
+          reinterpret_cast<float4*>(p.out)[at] = acc;
         } else {
-          w.x = lk_pack_f16x2(acc.x, acc.y);
-          w.y = lk_pack_f16x2(acc.z, acc.w);
+          uint2 w;
+          if (p.out_dtype == LK_BF16) {
+            w.x = lk_pack_bf16x2(acc.x, acc.y);
+            w.y = lk_pack_bf16x2(acc.z, acc.w);
+          } else {
+            w.x = lk_pack_f16x2(acc.x, acc.y);
+            w.y = lk_pack_f16x2(acc.z, acc.w);
+          }
+          reinterpret_cast<uint2*>(p.out)[at] = w;
         }
-        reinterpret_cast<uint2*>(p.out)[at] = w;
       }
+      if (threads >= vec) break;
     }
     return;
   }
   // ---- accumulated weights
-  const int i = blockIdx.x - n_out;
+  const int i = blockIdx.x - p.n_out;
   const int bh = i / p.mass_chunks, t0 = (i - bh * p.mass_chunks) * kMassTok;
   const int b = bh / p.n_kv, h = bh - b * p.n_kv;
   const int len = max(0, min(__ldcg(p.seq_len + b), p.max_len));
@@ -1128,7 +1140,11 @@ cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream)
   j.out_dtype = a.out_dtype;
   j.offset = dt == DT_BF16 ? 0.0f : kHeld;
   j.mass_chunks = a.accumulate ? (a.max_len + kMassTok - 1) / kMassTok : 0;
-  const unsigned ctas = (unsigned)(c.batch * a.n_heads) + (unsigned)(c.batch * c.n_kv_heads) * (unsigned)j.mass_chunks;
+  // about grid / units pieces a unit: one warp reads eight in two turns
+  j.wph = r.grid > 8 * r.units ? kJoinThreads / 32 : 1;
+  const int per_cta = (kJoinThreads / 32) / j.wph;
+  j.n_out = (c.batch * a.n_heads + per_cta - 1) / per_cta;
+  const unsigned ctas = (unsigned)j.n_out + (unsigned)(c.batch * c.n_kv_heads) * (unsigned)j.mass_chunks;
   return lk::launch_pdl(paged_join_kernel, dim3(ctas), dim3(kJoinThreads), stream, j);
 }
 
