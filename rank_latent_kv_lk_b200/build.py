@@ -4,8 +4,10 @@ Usage: python rank_latent_kv_lk_b200/build.py [--force] [--verbose] [--ptxas-inf
 (run as a script: importing the package would load the library it builds).
 
 Each .cu file compiles to an object under ``_build/`` (in parallel), then the
-objects link into ``rank_latent_kv_lk_b200/liblk.so``.  Objects are rebuilt
-when their source or any header is newer.  IEEE fp32 semantics are kept
+objects link into ``rank_latent_kv_lk_b200/liblk.so``; the torch binding of the
+serving operators (``csrc/lk_serving_py.cpp``) compiles with g++ into
+``_serving_ext.so`` beside it.  Objects are rebuilt when their source or any
+header is newer.  IEEE fp32 semantics are kept
 (no fast-math, no flush-to-zero): the latent quantiser is bit-exact.
 """
 from __future__ import annotations
@@ -24,6 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblk.so")
+EXT_SRC = os.path.join(CSRC, "lk_serving_py.cpp")
+EXT = os.path.join(PKG, "_serving_ext.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + [
@@ -56,6 +60,31 @@ def _compile(src, obj, verbose, extra):
     return p.stderr
 
 
+def _build_ext(force, verbose):
+    """The torch binding; links against liblk.so beside it."""
+    deps = [EXT_SRC, os.path.join(INCLUDE, "lk.h"), os.path.join(INCLUDE, "lk_serving.h")]
+    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(d) for d in deps):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"), *cpp_extension.include_paths()]
+    libs = cpp_extension.library_paths()
+    tmp = EXT + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-DTORCH_EXTENSION_NAME=_serving_ext",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in inc], EXT_SRC,
+           "-o", tmp, f"-L{PKG}", "-l:liblk.so", "-Wl,-rpath,$ORIGIN", *[f"-L{d}" for d in libs],
+           "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(EXT_SRC)}:\n{p.stdout}\n{p.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force=False, verbose=False, extra_flags=()):
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -80,6 +109,7 @@ def build(force=False, verbose=False, extra_flags=()):
         if p.returncode != 0:
             raise RuntimeError(f"link failed:\n{p.stdout}\n{p.stderr}")
         os.replace(tmp, LIB)
+    _build_ext(force, verbose)
     for log in logs:
         if log.strip() and verbose:
             print(log)

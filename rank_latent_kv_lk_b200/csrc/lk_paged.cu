@@ -70,6 +70,7 @@ struct PagedParams {
   float qscale;     // softmax_scale * log2(e)
   int n_pages, page_shift, n_kv, D, batch, width, group, nch, max_len, q_stride, q_f16;
   int hs;           // score rows per block
+  int resident;     // CTAs the GPU holds
 };
 
 // The reference a head's weights are taken relative to follows the running
@@ -119,9 +120,14 @@ LK_DEVICE void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   }
 }
 
-// CTAs that N blocks are dealt out to: each gets a block for every warp, and
-// none is empty (a unit's pieces are then consecutive CTAs).
-LK_DEVICE int64_t working_ctas(int64_t N, int grid) { return max((int64_t)1, min((int64_t)grid, N / kWarps)); }
+// CTAs that N blocks are dealt out to: all resident at once, each with a block
+// for every warp, none empty (a unit's pieces are then consecutive CTAs).
+// (More and smaller ranges, for SMs that are served faster to take more, cost
+// 4 to 10 % on long caches: their start-up is not hidden.)
+__host__ __device__ inline int64_t working_ctas(int64_t N, int64_t resident) {
+  const int64_t ctas = N / kWarps < resident ? N / kWarps : resident;
+  return ctas < 1 ? 1 : ctas;
+}
 
 // Blocks of one (head, chunk) of sequence b.
 LK_DEVICE int seq_blocks(const PagedParams& p, int b) {
@@ -163,10 +169,11 @@ struct Shape {
   static constexpr int kHP = 8 * NT;
   static constexpr int kOStride = VC * 64 + 4;
   static constexpr int kRowsPer = 32 / kCh;                          // rows a warp copies at a time
-  // Stages and CTAs an SM: about 64 KB (small rows) to 100 KB of ring a CTA
-  static constexpr int kStages = kStageB <= 6400 ? 4 : (kStageB <= 9000 ? 3 : (kStageB <= 12288 ? 2 : 3));
+  // Stages and CTAs an SM.  Rows of 256 bytes, one sequence of 4224 tokens: 2 stages and 3 CTAs 20.5 us, 3 and 2
+  // 22.1, 4 and 1 24.9; rows of 128 bytes, fp16 with weights: 2 and 5 29.1 us, 3 and 4 29.2, 4 and 3 30.2.
+  static constexpr int kStages = kStageB <= 2200 ? 4 : (kStageB <= 12288 ? 2 : 3);
   static constexpr int kRingB = kStages * kStageB;
-  static constexpr int kMinCtas = kRingB * kWarps <= 36 * 1024 ? 4 : (kRingB * kWarps <= 68 * 1024 ? 3 : (kRingB * kWarps <= 104 * 1024 ? 2 : 1));
+  static constexpr int kMinCtas = kStageB <= 2200 ? 4 : kStageB <= 4300 ? (NT == 1 ? 5 : 3) : (kStageB <= 9000 ? 3 : (kStageB <= 12288 ? 2 : 1));
   static constexpr int kQB = NT * (kSteps / 2) * 32 * 16;
   static constexpr int kSmem = kWarps * kRingB + kQB;
   static_assert(kHP * kOStride * 4 <= kRingB, "a warp's partial fits in its ring");
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
     const int64_t N = (int64_t)tot * per_seq;
-    const int64_t first = (int64_t)blockIdx.x * N / working_ctas(N, gridDim.x);
+    const int64_t first = (int64_t)blockIdx.x * N / working_ctas(N, p.resident);
     int run = 0;
     if (lane == 0) sh[0] = p.batch;
     __syncwarp();
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
   __syncthreads();
   {
     const int64_t N = (int64_t)sh[2] * per_seq;
-    const int64_t G = working_ctas(N, gridDim.x);
+    const int64_t G = working_ctas(N, p.resident);
     if (blockIdx.x >= G) return;
     i0 = (int64_t)blockIdx.x * N / G;
     i1 = (int64_t)(blockIdx.x + 1) * N / G;
@@ -664,7 +671,7 @@ struct JoinParams {
   const int32_t* table;
   const int32_t* seq_len;
   void* out;
-  int grid;  // CTAs of the split kernel
+  int resident;  // CTAs of the split kernel the GPU holds
   int n_pages, page_shift, n_kv, D, batch, width, group, nch, max_len, hp, hs, out_dtype, mass_chunks;
   int n_out, wph;  // CTAs for the outputs, warps a head
   float offset;  // log2 of the factor the sums are held with
@@ -676,7 +683,7 @@ struct Pieces {
 };
 LK_DEVICE Pieces unit_pieces(const JoinParams& p, int64_t start, int nb, int64_t N) {
   Pieces r;
-  const int64_t G = working_ctas(N, p.grid);
+  const int64_t G = working_ctas(N, p.resident);
   r.c0 = (int)(((start + 1) * G - 1) / N);
   r.c1 = (int)(((start + nb) * G - 1) / N);
   return r;
@@ -992,7 +999,7 @@ int heads_per_chunk(int group, int D) { return group > 8 && D <= 128 ? 16 : 8; }
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Plan {
-  int hp, nch, units, hs, vc, nt, grid;
+  int hp, nch, units, hs, vc, nt, grid, resident;
   int64_t blocks;
   size_t off_stats, off_part, off_scores, bytes;
 };
@@ -1025,9 +1032,8 @@ Plan make_plan(int batch, int n_kv, int n_heads, int D, int dtype, int max_len, 
   r.units = batch * n_kv * r.nch;
   r.hs = std::min(group, r.hp);
   r.blocks = (int64_t)r.units * ((max_len + kTok - 1) / kTok);
-  // every warp of a CTA gets a block, and the grid is resident at once
-  r.grid = (int)std::max<int64_t>(
-      1, std::min<int64_t>((int64_t)num_sms * ctas_per_sm(r.vc, r.nt, dt), (r.blocks + kWarps - 1) / kWarps));
+  r.resident = num_sms * ctas_per_sm(r.vc, r.nt, dt);
+  r.grid = (int)working_ctas(r.blocks, r.resident);
   const size_t slots = (size_t)r.grid + r.units;
   r.off_stats = round256((size_t)(batch + 1) * 4);
   r.off_part = r.off_stats + round256(slots * r.hp * 2 * 4);
@@ -1106,6 +1112,7 @@ cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream)
   p.q_stride = a.q_stride;
   p.q_f16 = a.q_f16;
   p.hs = r.hs;
+  p.resident = r.resident;
   cudaError_t e;
   switch (r.vc * 2 + (r.nt - 1)) {
     case 2: e = launch_split<1, 1>(dt, r.grid, p, stream); break;
@@ -1125,7 +1132,7 @@ cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream)
   j.table = p.table;
   j.seq_len = p.seq_len;
   j.out = a.out;
-  j.grid = r.grid;
+  j.resident = r.resident;
   j.n_pages = p.n_pages;
   j.page_shift = p.page_shift;
   j.n_kv = p.n_kv;
