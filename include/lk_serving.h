@@ -93,7 +93,9 @@ lk_status lk_paged_append(const lk_paged_cache* cache, const int32_t* page_table
  *   any contents; calls that may run at the same time need their own.
  * Scores, softmax statistics and the output sum are fp32; the weights p meet
  *   V as a sum of two 16-bit terms (relative rounding at most 2^-16).
- *   Results do not depend on timing.  Two launches.
+ *   Results do not depend on timing.  One launch for a max_seq_len of up to
+ *   512 (for accumulate: and a group of at most 8 heads, 16 up to head_dim
+ *   128), else two.
  */
 lk_status lk_paged_decode_attn(const lk_paged_cache* cache, const int32_t* page_table, int32_t batch,
                                int32_t table_width, const void* q, lk_dtype q_dtype, int32_t n_heads,

@@ -71,6 +71,11 @@ struct PagedParams {
   int n_pages, page_shift, n_kv, D, batch, width, group, nch, max_len, q_stride, q_f16;
   int hs;           // score rows per block
   int resident;     // CTAs the GPU holds
+  // one CTA a unit (grid = units): the output and mass are written here
+  int direct, unit_blocks, out_dtype;
+  void* out;
+  float* mass;
+  float offset;     // log2 of the factor weights and sums are held with
 };
 
 // The reference a head's weights are taken relative to follows the running
@@ -123,10 +128,42 @@ LK_DEVICE void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
 // CTAs that N blocks are dealt out to: all resident at once, each with a block
 // for every warp, none empty (a unit's pieces are then consecutive CTAs).
 // (More and smaller ranges, for SMs that are served faster to take more, cost
-// 4 to 10 % on long caches: their start-up is not hidden.)
+// 4 to 10 % on long caches: their start-up is not hidden.  Ranges that end
+// with a unit where all sequences are equally long gain nothing.)
 __host__ __device__ inline int64_t working_ctas(int64_t N, int64_t resident) {
   const int64_t ctas = N / kWarps < resident ? N / kWarps : resident;
   return ctas < 1 ? 1 : ctas;
+}
+
+// a / c of numbers that are not negative, in 32 bits where they fit (a 64-bit division is 0.2 us on the way to a
+// CTA's first load).
+LK_DEVICE int64_t quotient(int64_t a, int64_t c) {
+  if (((a | c) >> 32) == 0) return (uint32_t)a / (uint32_t)c;
+  return a / c;
+}
+
+// Four outputs in the call's type.
+LK_DEVICE void store_out(void* out, int64_t at, const float4& v, int dtype) {
+  if (dtype == LK_F32) {
+    reinterpret_cast<float4*>(out)[at] = v;
+  } else {
+    uint2 w;
+    if (dtype == LK_BF16) {
+      w.x = lk_pack_bf16x2(v.x, v.y);
+      w.y = lk_pack_bf16x2(v.z, v.w);
+    } else {
+      w.x = lk_pack_f16x2(v.x, v.y);
+      w.y = lk_pack_f16x2(v.z, v.w);
+    }
+    reinterpret_cast<uint2*>(out)[at] = w;
+  }
+}
+
+// The output of an empty sequence.
+LK_DEVICE void zero_rows(const PagedParams& p, int b, int tid, int threads) {
+  const int n = p.n_kv * p.group * (p.D / 4);
+  for (int i = tid; i < n; i += threads)
+    store_out(p.out, (int64_t)b * n + i, make_float4(0.0f, 0.0f, 0.0f, 0.0f), p.out_dtype);
 }
 
 // Blocks of one (head, chunk) of sequence b.
@@ -194,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
   extern __shared__ __align__(128) uint8_t smem[];
   uint4 (*Qs)[S::kSteps / 2][32] = reinterpret_cast<uint4 (*)[S::kSteps / 2][32]>(smem + kWarps * S::kRingB);
   __shared__ float mst[kWarps][S::kHP][2];
+  __shared__ float unit_st[S::kHP][2];
   __shared__ float qf[S::kHP];
   __shared__ int sh[4];  // sequence, its first block, blocks in all, blocks of this sequence
 
@@ -208,48 +246,59 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
 
   // blocks in all, then this CTA's range and the sequence it starts in
   int64_t i0, i1;
-  if (warp == 0) {
-    int tot = 0;
-    for (int b = lane; b < p.batch; b += 32) tot += seq_blocks(p, b);
+  int b, b_start, nb;
+  if (p.direct) {
+    b = blockIdx.x / per_seq;
+    b_start = 0;
+    nb = seq_blocks(p, b);
+    const int hc = blockIdx.x - b * per_seq;
+    i0 = (int64_t)hc * nb;
+    i1 = i0 + nb;
+    if (nb == 0 && hc == 0) zero_rows(p, b, threadIdx.x, kThreads);
+  } else {
+    if (warp == 0) {
+      int tot = 0;
+      for (int e = lane; e < p.batch; e += 32) tot += seq_blocks(p, e);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    const int64_t N = (int64_t)tot * per_seq;
-    const int64_t first = (int64_t)blockIdx.x * N / working_ctas(N, p.resident);
-    int run = 0;
-    if (lane == 0) sh[0] = p.batch;
-    __syncwarp();
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      const int b = b0 + lane;
-      const int nb = b < p.batch ? seq_blocks(p, b) : 0;
-      int inc = nb;
+      for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+      const int64_t N = (int64_t)tot * per_seq;
+      const int64_t first = quotient(blockIdx.x * N, working_ctas(N, p.resident));
+      int run = 0;
+      if (lane == 0) sh[0] = p.batch;
+      __syncwarp();
+      for (int e0 = 0; e0 < p.batch; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = e < p.batch ? seq_blocks(p, e) : 0;
+        int inc = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += x;
+        }
+        const int at = run + inc - n;
+        if (blockIdx.x == 0 && e < p.batch) p.starts[e] = at;
+        if (n > 0 && first >= (int64_t)at * per_seq && first < (int64_t)(at + n) * per_seq) {
+          sh[0] = e;
+          sh[1] = at;
+          sh[3] = n;
+        }
+        run += __shfl_sync(0xffffffffu, inc, 31);
       }
-      const int at = run + inc - nb;
-      if (blockIdx.x == 0 && b < p.batch) p.starts[b] = at;
-      if (nb > 0 && first >= (int64_t)at * per_seq && first < (int64_t)(at + nb) * per_seq) {
-        sh[0] = b;
-        sh[1] = at;
-        sh[3] = nb;
+      if (lane == 0) {
+        sh[2] = tot;
+        if (blockIdx.x == 0) p.starts[p.batch] = tot;
       }
-      run += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) {
-      sh[2] = tot;
-      if (blockIdx.x == 0) p.starts[p.batch] = tot;
-    }
-  }
-  __syncthreads();
-  {
+    __syncthreads();
     const int64_t N = (int64_t)sh[2] * per_seq;
     const int64_t G = working_ctas(N, p.resident);
     if (blockIdx.x >= G) return;
-    i0 = (int64_t)blockIdx.x * N / G;
-    i1 = (int64_t)(blockIdx.x + 1) * N / G;
+    i0 = quotient(blockIdx.x * N, G);
+    i1 = quotient((blockIdx.x + 1) * N, G);
+    b = sh[0];
+    b_start = sh[1];
+    nb = sh[3];
   }
-  int b = sh[0], b_start = sh[1], nb = sh[3];
 
   while (i0 < i1) {
     while (i0 >= (int64_t)(b_start + nb) * per_seq) {  // next sequence with tokens
@@ -396,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
     const uint32_t f_at = f_row * S::kRowB;
     const uint32_t f_ch = ((lane >> 4) ^ swizzle<S::kCh>(f_row)) << 4;
     // the block's scores of heads 2 tig, tokens gid
-    float* sp = p.scores + (((int64_t)b_start * per_seq + (int64_t)hc * nb + blk) * p.hs + 2 * tig) * kTok + gid;
+    const int64_t first_block = p.direct ? (int64_t)unit * p.unit_blocks : (int64_t)b_start * per_seq + (int64_t)hc * nb;
+    float* sp = p.scores + ((first_block + blk) * p.hs + 2 * tig) * kTok + gid;
     for (; blk < s1; blk += kWarps, sp += kWarps * p.hs * kTok) {
       // ---- request the block S::kStages - 1 ahead, then wait for this one
       {
@@ -641,10 +691,32 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
         // a NaN score leaves the maximum alone; its sum carries it on
         L = fmaf(f, mst[w][j][1], L);
       }
-      *reinterpret_cast<float4*>(p.part + (slot * S::kHP + j) * D + d) = acc;
-      if (d == 0) {
-        p.stats[(slot * S::kHP + j) * 2] = M;
-        p.stats[(slot * S::kHP + j) * 2 + 1] = L;
+      if (p.direct) {
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;  // every score -infinity: zeros
+        store_out(p.out, ((int64_t)b * p.n_kv * p.group + h * p.group + n0) * (D / 4) + i,
+                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.out_dtype);
+        if (d == 0) {
+          unit_st[j][0] = M == -INFINITY ? 0.0f : M;
+          unit_st[j][1] = L == 0.0f ? 0.0f : exp2f(p.offset) / L;
+        }
+      } else {
+        *reinterpret_cast<float4*>(p.part + (slot * S::kHP + j) * D + d) = acc;
+        if (d == 0) {
+          p.stats[(slot * S::kHP + j) * 2] = M;
+          p.stats[(slot * S::kHP + j) * 2 + 1] = L;
+        }
+      }
+    }
+    if (p.direct && p.scores) {  // (a single chunk of heads)
+      __syncthreads();
+      for (int t = threadIdx.x; t < len; t += kThreads) {
+        const int row = lk_paged_row(__ldcg(trow + (t >> p.page_shift)), t, h, p.n_pages, p.n_kv, p.page_shift);
+        if (row < 0) continue;
+        const float* src = p.scores + (first_block + t / kTok) * p.hs * kTok + t % kTok;
+        float add = 0.0f;
+#pragma unroll 4
+        for (int j = 0; j < heads; ++j) add = fmaf(ex2(__ldcg(src + j * kTok) - unit_st[j][0]), unit_st[j][1], add);
+        p.mass[row] = __ldcg(p.mass + row) + add;
       }
     }
     __syncthreads();
@@ -684,8 +756,8 @@ struct Pieces {
 LK_DEVICE Pieces unit_pieces(const JoinParams& p, int64_t start, int nb, int64_t N) {
   Pieces r;
   const int64_t G = working_ctas(N, p.resident);
-  r.c0 = (int)(((start + 1) * G - 1) / N);
-  r.c1 = (int)(((start + nb) * G - 1) / N);
+  r.c0 = (int)quotient((start + 1) * G - 1, N);
+  r.c1 = (int)quotient((start + nb) * G - 1, N);
   return r;
 }
 
@@ -784,19 +856,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         acc.z *= inv;
         acc.w *= inv;
         const int64_t at = (int64_t)head * vec + d;
-        if (p.out_dtype == LK_F32) {
-          reinterpret_cast<float4*>(p.out)[at] = acc;
-        } else {
-          uint2 w;
-          if (p.out_dtype == LK_BF16) {
-            w.x = lk_pack_bf16x2(acc.x, acc.y);
-            w.y = lk_pack_bf16x2(acc.z, acc.w);
-          } else {
-            w.x = lk_pack_f16x2(acc.x, acc.y);
-            w.y = lk_pack_f16x2(acc.z, acc.w);
-          }
-          reinterpret_cast<uint2*>(p.out)[at] = w;
-        }
+        store_out(p.out, at, acc, p.out_dtype);
       }
       if (threads >= vec) break;
     }
@@ -996,10 +1056,15 @@ int log2_of(int x) {
 // accumulators of 16 heads still fit.
 int heads_per_chunk(int group, int D) { return group > 8 && D <= 128 ? 16 : 8; }
 
+// Up to here a unit is one CTA's (one launch, no join).  32 units of 256-byte rows: 512 tokens 8.7 us against 9.4 of
+// the split, 768 tokens 11.3 against 9.6; 128 units: 10.2 against 14.5 and 13.8 against 18.4.
+constexpr int kDirect = 512;
+
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Plan {
-  int hp, nch, units, hs, vc, nt, grid, resident;
+  int hp, nch, units, hs, vc, nt, grid, resident, unit_blocks;
+  bool direct;
   int64_t blocks;
   size_t off_stats, off_part, off_scores, bytes;
 };
@@ -1034,6 +1099,14 @@ Plan make_plan(int batch, int n_kv, int n_heads, int D, int dtype, int max_len, 
   r.blocks = (int64_t)r.units * ((max_len + kTok - 1) / kTok);
   r.resident = num_sms * ctas_per_sm(r.vc, r.nt, dt);
   r.grid = (int)working_ctas(r.blocks, r.resident);
+  r.unit_blocks = (max_len + kTok - 1) / kTok;
+  r.direct = max_len <= kDirect && (!accumulate || r.nch == 1);
+  if (r.direct) {
+    r.grid = r.units;
+    r.off_stats = r.off_part = r.off_scores = 0;
+    r.bytes = accumulate ? (size_t)r.blocks * r.hs * kTok * 4 : 1;
+    return r;
+  }
   const size_t slots = (size_t)r.grid + r.units;
   r.off_stats = round256((size_t)(batch + 1) * 4);
   r.off_part = r.off_stats + round256(slots * r.hp * 2 * 4);
@@ -1113,6 +1186,12 @@ cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream)
   p.q_f16 = a.q_f16;
   p.hs = r.hs;
   p.resident = r.resident;
+  p.direct = r.direct;
+  p.unit_blocks = r.unit_blocks;
+  p.out = a.out;
+  p.out_dtype = a.out_dtype;
+  p.mass = a.accumulate ? c.mass : nullptr;
+  p.offset = dt == DT_BF16 ? 0.0f : kHeld;
   cudaError_t e;
   switch (r.vc * 2 + (r.nt - 1)) {
     case 2: e = launch_split<1, 1>(dt, r.grid, p, stream); break;
@@ -1122,7 +1201,7 @@ cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream)
     case 6: e = launch_split<3, 1>(dt, r.grid, p, stream); break;
     default: e = launch_split<4, 1>(dt, r.grid, p, stream); break;
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || r.direct) return e;
   JoinParams j{};
   j.starts = p.starts;
   j.stats = p.stats;
@@ -1145,7 +1224,7 @@ cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream)
   j.hp = r.hp;
   j.hs = r.hs;
   j.out_dtype = a.out_dtype;
-  j.offset = dt == DT_BF16 ? 0.0f : kHeld;
+  j.offset = p.offset;
   j.mass_chunks = a.accumulate ? (a.max_len + kMassTok - 1) / kMassTok : 0;
   // about grid / units pieces a unit: one warp reads eight in two turns
   j.wph = r.grid > 8 * r.units ? kJoinThreads / 32 : 1;
