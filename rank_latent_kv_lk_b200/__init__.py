@@ -18,7 +18,9 @@ _SERVING = ("PagedKVCache", "paged_append", "paged_decode_attn", "paged_evict", 
 
 def __getattr__(name):
     if name in _SERVING:
-        return getattr(importlib.import_module(".serving", __name__), name)
+        value = getattr(importlib.import_module(".serving", __name__), name)
+        globals()[name] = value  # found at once from now on: this look-up costs a microsecond a call
+        return value
     if name in _API:
         return getattr(importlib.import_module(".api", __name__), name)
     if name == "LkError":

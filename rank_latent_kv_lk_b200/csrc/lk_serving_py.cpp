@@ -8,6 +8,7 @@
 #include <torch/extension.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -68,9 +69,11 @@ lk_stream_t stream_of(const at::Device& dev) {
   return reinterpret_cast<lk_stream_t>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
 }
 
-Tensor scratch(size_t bytes, const at::Device& dev) {
-  return at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
+// An uninitialised tensor from torch's allocator (without the dispatcher's microsecond).
+Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
+  return Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
 }
+Tensor scratch(size_t bytes, const at::Device& dev) { return empty({(int64_t)bytes}, at::kByte, dev); }
 
 struct PagedCache {
   Tensor k, v;
@@ -173,8 +176,7 @@ Tensor paged_decode_attn(const PagedCache& c, const Tensor& table, const Tensor&
   const int32_t width = c.width(table, batch);
   c.counts("seq_len", seq_len, batch);
   if (out) same("out", *out, q.sizes(), out->scalar_type(), c.dev);
-  Tensor o = out ? *out
-                 : at::empty(q.sizes(), at::TensorOptions().dtype(out_dtype.value_or(q.scalar_type())).device(c.dev));
+  Tensor o = out ? *out : empty(q.sizes(), out_dtype.value_or(q.scalar_type()), c.dev);
   const lk_dtype qt = dtype_of("q", q.scalar_type(), true), ot = dtype_of("out", o.scalar_type(), false);
   const int32_t b = as_i32("batch", batch), h = as_i32("n_heads", heads), m = as_i32("max_seq_len", max_seq_len);
   const size_t need = lk_paged_decode_workspace_bytes(&c.d, b, h, m, accumulate);
@@ -249,7 +251,7 @@ Tensor w4_linear(const W4& w, const Tensor& x, const OptTensor& residual, const 
   const int64_t shape[2] = {m, w.n_out};
   same("residual", residual, shape, x.scalar_type(), w.dev);
   if (y) same("y", *y, shape, y->scalar_type(), w.dev);
-  Tensor o = y ? *y : at::empty(shape, at::TensorOptions().dtype(y_dtype.value_or(x.scalar_type())).device(w.dev));
+  Tensor o = y ? *y : empty(shape, y_dtype.value_or(x.scalar_type()), w.dev);
   check(lk_w4_linear(ptr(w.packed), w.n_out, w.k_in, w.group, w.gated, ptr(x),
                      dtype_of("x", x.scalar_type(), true), as_i32("m", m),
                      as_i32("stride of x", m > 1 ? x.stride(0) : w.k_in), ptr(residual), ptr(o),
@@ -276,10 +278,9 @@ std::pair<Tensor, OptTensor> rmsnorm_gate_residual(const Tensor& y, const Tensor
   same("x_out", x_out, shape, t, dev);
   same("h", h, shape, t, dev);
   TORCH_CHECK_VALUE(w_pre.has_value() || !h.has_value(), "h needs w_pre");
-  const auto opt = at::TensorOptions().dtype(t).device(dev);
-  Tensor xo = x_out ? *x_out : at::empty(shape, opt);
+  Tensor xo = x_out ? *x_out : empty(shape, t, dev);
   OptTensor ho = h;
-  if (w_pre && !h) ho = at::empty(shape, opt);
+  if (w_pre && !h) ho = empty(shape, t, dev);
   if (shape[0] > 0)
     check(lk_rmsnorm_gate_residual(ptr(y), ptr(x), ptr(w_post), ptr(gate), per_row, ptr(w_pre), dt,
                                    as_i32("m", shape[0]), as_i32("width", shape[1]), (float)scale, (float)eps, ptr(xo),

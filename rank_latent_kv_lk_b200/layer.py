@@ -14,6 +14,10 @@ layer with unit RMSNorm weights, eps 1e-5, no positional rotation):
   out      = x2 + hybrid(m_q; down)
 
 Every step is a call into the C ABI; this module only wires buffers.
+
+W4PagedDecoderLayer is its neighbour for layers whose K and V stay dense: 4-bit
+weights, grouped heads over a paged key-value cache, eviction by accumulated
+attention weight, and the norms around a block fused with its residual.
 """
 from __future__ import annotations
 
@@ -21,6 +25,8 @@ import torch
 
 from .api import (LatentCache, LowrankWeight, latent_decode_step, lowrank_linear, quantize_rows_i8,
                   rmsnorm_quant_i8, swiglu_quant_i8)
+from .serving import (PagedKVCache, W4Weight, paged_append, paged_decode_attn, paged_evict, rmsnorm_gate_residual,
+                      w4_linear)
 
 
 def dense_weight(W, s, device):
@@ -79,3 +85,53 @@ class W8A8DecoderLayer:
             trace.update(xq=xq, sx=sx, q=q, attn=attn, aq=aq, sa=sa, x2=x2, hq=hq, sh=sh, gate=g, up=u, mq=mq,
                          sm=sm, out=out)
         return out
+
+
+class W4PagedDecoderLayer:
+    """One pre-norm decoder layer with 4-bit weights and a paged K/V cache.
+
+    step(): h is the normed input (the previous layer's second result, or
+    rmsnorm_gate_residual of the embedding), x the residual stream:
+
+      q, k, v  = h W_QKV^T                     (4-bit; k, v appended to the pages)
+      a        = attention over the pages      (weights accumulated if the cache has mass)
+      x, h     = x + g_1 . post_1(a W_O^T),  RMSNorm . w_ffn
+      m        = silu(h W_gate^T) * (h W_up^T) (4-bit, one launch)
+      x, h     = x + g_2 . post_2(m W_down^T), RMSNorm . w_next
+
+    weights: (codes, scales) for "qkv" [(n_heads + 2 n_kv_heads) head_dim, E],
+    "o", "gate", "up", "down" (codes and scales as W4Weight); [E] tensors
+    "norm_ffn", "norm_next" and optionally "post_attn", "post_ffn" (norms
+    behind a block) and "gate_attn", "gate_ffn" (its gate).
+    """
+
+    def __init__(self, weights, n_heads, n_kv_heads, head_dim, n_pages, page_size, cache_dtype=torch.bfloat16,
+                 mass=False, eps=1e-5, device="cuda"):
+        self.n_heads, self.n_kv_heads, self.head_dim, self.eps = n_heads, n_kv_heads, head_dim, eps
+
+        def w4(*names):
+            return W4Weight(*[t.to(device) for n in names for t in weights[n]])
+
+        self.qkv, self.o, self.gate_up, self.down = w4("qkv"), w4("o"), w4("gate", "up"), w4("down")
+        self.norm = {k: None if weights.get(k) is None else weights[k].to(device)
+                     for k in ("norm_ffn", "norm_next", "post_attn", "post_ffn", "gate_attn", "gate_ffn")}
+        self.cache = PagedKVCache(n_pages, page_size, n_kv_heads, head_dim, cache_dtype, mass, device)
+
+    def step(self, x, h, page_table, seq_len, max_seq_len, next_pos=None):
+        """x, h: [B, E]; page_table, seq_len, next_pos: device int32 (lengths and positions advance by one in
+        place); max_seq_len: host bound on the lengths after the step."""
+        B, nh, nk, D, n = x.shape[0], self.n_heads, self.n_kv_heads, self.head_dim, self.norm
+        qkv = w4_linear(self.qkv, h)
+        q = qkv[:, :nh * D].view(B, nh, D)
+        k = qkv[:, nh * D:(nh + nk) * D].view(B, 1, nk, D)
+        v = qkv[:, (nh + nk) * D:].view(B, 1, nk, D)
+        paged_append(self.cache, page_table, k, v, seq_len, next_pos)
+        a = paged_decode_attn(self.cache, page_table, q, seq_len, max_seq_len, accumulate=self.cache.mass is not None)
+        y = w4_linear(self.o, a.view(B, nh * D))
+        x, h = rmsnorm_gate_residual(y, x, n["post_attn"], n["gate_attn"], 1.0, n["norm_ffn"], self.eps)
+        y = w4_linear(self.down, w4_linear(self.gate_up, h))
+        return rmsnorm_gate_residual(y, x, n["post_ffn"], n["gate_ffn"], 1.0, n["norm_next"], self.eps)
+
+    def evict(self, page_table, seq_len, next_pos, max_seq_len, budget, window=0, n_sink=0):
+        """Cut the sequences to `budget` cached tokens per kv head (lengths in place)."""
+        paged_evict(self.cache, page_table, seq_len, next_pos, max_seq_len, budget, window, n_sink)
