@@ -43,14 +43,15 @@
 //
 // Masked slots (behind the length, or on a page outside the pool) are not
 // read: their K and V are zero-filled and their score is -infinity.
+#include <algorithm>
 #include <atomic>
 
 #include "lk_serving.cuh"
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 4;  // of a CTA of the split
+constexpr int kWideStage = 12 * 1024 + 128;  // largest stage of a CTA of eight warps (two of them each fit)
 constexpr int kTok = 16;  // tokens per block
 
 enum { DT_BF16 = 0, DT_F16 = 1, DT_I8 = 2 };
@@ -73,6 +74,7 @@ struct PagedParams {
   int resident;     // CTAs the GPU holds
   // one CTA a unit (grid = units): the output and mass are written here
   int direct, unit_blocks, out_dtype;
+  int ring;         // bytes of a warp's ring
   void* out;
   float* mass;
   float offset;     // log2 of the factor weights and sums are held with
@@ -195,8 +197,8 @@ LK_DEVICE void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "memory");
 }
 
-// Head dims up to 64 VC, 8 NT heads.
-template <int VC, int NT, int DT>
+// Head dims up to 64 VC, 8 NT heads, W warps.
+template <int VC, int NT, int DT, int W>
 struct Shape {
   static constexpr int kCh = VC * 64 * (DT == DT_I8 ? 1 : 2) / 16;  // 16-byte chunks of a row
   static constexpr int kRowB = kCh * 16;
@@ -209,11 +211,13 @@ struct Shape {
   // Stages and CTAs an SM.  Rows of 256 bytes, one sequence of 4224 tokens: 2 stages and 3 CTAs 20.5 us, 3 and 2
   // 22.1, 4 and 1 24.9; rows of 128 bytes, fp16 with weights: 2 and 5 29.1 us, 3 and 4 29.2, 4 and 3 30.2.
   static constexpr int kStages = kStageB <= 2200 ? 4 : (kStageB <= 12288 ? 2 : 3);
-  static constexpr int kRingB = kStages * kStageB;
-  static constexpr int kMinCtas = kStageB <= 2200 ? 4 : kStageB <= 4300 ? (NT == 1 ? 5 : 3) : (kStageB <= 9000 ? 3 : (kStageB <= 12288 ? 2 : 1));
+  static constexpr int kMinCtas =
+      W > kWarps ? 1 : (kStageB <= 2200 ? 4 : kStageB <= 4300 ? (NT == 1 ? 5 : 3) : (kStageB <= 9000 ? 3 : (kStageB <= 12288 ? 2 : 1)));
   static constexpr int kQB = NT * (kSteps / 2) * 32 * 16;
-  static constexpr int kSmem = kWarps * kRingB + kQB;
-  static_assert(kHP * kOStride * 4 <= kRingB, "a warp's partial fits in its ring");
+  static constexpr int kPartialB = kHP * kOStride * 4;
+  // A warp's ring: no more stages than it has blocks, and room for its partial.
+  static int ring(int blocks) { return std::max(std::min(kStages, std::max(blocks, 1)) * kStageB, (kPartialB + 127) / 128 * 128); }
+  static int smem(int blocks) { return W * ring(blocks) + kQB; }
   static_assert(kStages <= 4, "live masks of the stages fit in 64 bits");
 };
 
@@ -224,12 +228,14 @@ LK_DEVICE int swizzle(int row) {
   return CH % 8 == 0 ? row & 7 : (row >> 1) & 3;
 }
 
-template <int VC, int NT, int DT>
-__global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
+// FULL: the head dim is 64 VC (else products behind it are skipped).
+template <int VC, int NT, int DT, int W, bool FULL>
+__global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
     paged_decode_kernel(const __grid_constant__ PagedParams p) {
-  using S = Shape<VC, NT, DT>;
+  using S = Shape<VC, NT, DT, W>;
+  constexpr int kThreads = W * 32, kWarps = W;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint4 (*Qs)[S::kSteps / 2][32] = reinterpret_cast<uint4 (*)[S::kSteps / 2][32]>(smem + kWarps * S::kRingB);
+  uint4 (*Qs)[S::kSteps / 2][32] = reinterpret_cast<uint4 (*)[S::kSteps / 2][32]>(smem + kWarps * p.ring);
   __shared__ float mst[kWarps][S::kHP][2];
   __shared__ float unit_st[S::kHP][2];
   __shared__ float qf[S::kHP];
@@ -237,9 +243,11 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gid = lane >> 2, tig = lane & 3;
-  const int D = p.D, rows_b = DT == DT_I8 ? D : 2 * D;
+  const int D = FULL ? VC * 64 : p.D, rows_b = DT == DT_I8 ? D : 2 * D;
   const int per_seq = p.n_kv * p.nch;
-  uint8_t* ring = smem + warp * S::kRingB;
+  // products along the head dim; what a row's padding holds is not used
+  const int steps = FULL ? S::kSteps : D / 16;
+  uint8_t* ring = smem + warp * p.ring;
   const uint32_t ring_a = lk_smem_addr(ring);
   lk_grid_dep_wait();
   lk_grid_dep_launch();
@@ -325,17 +333,17 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
     };
     // copies a block's rows into a stage; lane l holds the row of token l % 16
     const int c_row = lane / S::kCh, c_ch = lane - c_row * S::kCh;
-    const bool c_in = c_row < S::kRowsPer;
+    const bool c_in = (FULL && S::kRowsPer * S::kCh == 32) || (c_row < S::kRowsPer && 16 * c_ch < rows_b);
     auto issue = [&](int stage, int row) {
       const uint32_t st = ring_a + stage * S::kStageB;
 #pragma unroll
       for (int i = 0; i < kTok / S::kRowsPer; ++i) {
         const int t = i * S::kRowsPer + (c_in ? c_row : 0);
         const int r = __shfl_sync(0xffffffffu, row, t);
-        const bool live = r >= 0 && 16 * c_ch < rows_b;
+        const bool live = r >= 0;
         const int64_t off = live ? (int64_t)r * rows_b + 16 * c_ch : 0;
         const uint32_t dst = st + t * S::kRowB + ((c_ch ^ swizzle<S::kCh>(t)) << 4);
-        if (S::kRowsPer * S::kCh == 32 || c_in) {
+        if (c_in) {
           cp_async16_zfill(dst, p.k + off, live);
           cp_async16_zfill(dst + kTok * S::kRowB, p.v + off, live);
         }
@@ -349,23 +357,19 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
     // The same for 16 live tokens of one page: their rows are consecutive, so
     // the addresses are one base and constant steps.
     const uint32_t c_dst = c_row * S::kRowB + ((c_ch ^ swizzle<S::kCh>(c_row)) << 4);
-    const bool c_live = 16 * c_ch < rows_b;
     auto issue_page = [&](int stage, int row) {
       const uint32_t st = ring_a + stage * S::kStageB;
-      const int64_t off = (int64_t)__shfl_sync(0xffffffffu, row, 0) * rows_b + (c_live ? c_row * rows_b + 16 * c_ch : 0);
+      const int64_t off = (int64_t)__shfl_sync(0xffffffffu, row, 0) * rows_b + (c_in ? c_row * rows_b + 16 * c_ch : 0);
       const uint8_t* ks = p.k + off;
       const uint8_t* vs = p.v + off;
-      if (S::kRowsPer * S::kCh == 32 || c_in) {
+      if (c_in) {
 #pragma unroll
         for (int i = 0; i < kTok / S::kRowsPer; ++i) {
           const uint32_t dst = st + i * S::kRowsPer * S::kRowB + (c_dst ^ (swizzle<S::kCh>(i * S::kRowsPer) << 4));
-          if (rows_b == S::kRowB) {
-            cp_async16(dst, ks + i * S::kRowsPer * S::kRowB);
-            cp_async16(dst + kTok * S::kRowB, vs + i * S::kRowsPer * S::kRowB);
-          } else {
-            cp_async16_zfill(dst, ks + i * S::kRowsPer * rows_b, c_live);
-            cp_async16_zfill(dst + kTok * S::kRowB, vs + i * S::kRowsPer * rows_b, c_live);
-          }
+          // (constant offsets where the rows fill the chunks)
+          const int step = rows_b == S::kRowB ? i * S::kRowsPer * S::kRowB : i * S::kRowsPer * rows_b;
+          cp_async16(dst, ks + step);
+          cp_async16(dst + kTok * S::kRowB, vs + step);
         }
       }
       if constexpr (DT == DT_I8)
@@ -395,7 +399,12 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
         float f = 1.0f;
         if (!p.q_f16) {
           float a = 0.0f;
-          for (int d = lane; d < D; d += 32) a = fmaxf(a, fabsf(lk_bf16_to_f32(__ldcg(src + d))));
+          if (8 * lane < D) {
+            const uint4 w = __ldcg(reinterpret_cast<const uint4*>(src) + lane);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a = fmaxf(a, fmaxf(fabsf(lk_bf16lo(u[e])), fabsf(lk_bf16hi(u[e]))));
+          }
           a = lk_warp_max(a);
           // 2^(14 - exponent of the largest), within fp32's normal range
           const int e = (int)(__float_as_uint(a) >> 23);
@@ -472,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
       for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.0f;
 #pragma unroll
       for (int v = 0; v < S::kSteps / 2; ++v) {
+        if (2 * v >= steps) break;
         uint4 qv[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) qv[nt] = Qs[nt][v][lane];
@@ -485,11 +495,12 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
             const uint32_t a1 = codes_f16<0x4140>(y), a3 = codes_f16<0x4342>(y);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816<DT>(c[nt], a0, a1, a2, a3, i ? qv[nt].z : qv[nt].x, i ? qv[nt].w : qv[nt].y);
+              if (2 * v + i < steps) mma16816<DT>(c[nt], a0, a1, a2, a3, i ? qv[nt].z : qv[nt].x, i ? qv[nt].w : qv[nt].y);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
+            if (2 * v + i >= steps) break;
             uint32_t k4[4];
             ldmatrix4<false>(k4, st + f_at + (f_ch ^ ((2 * v + i) << 5)));
 #pragma unroll
@@ -611,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
       // ---- weighted V
 #pragma unroll
       for (int v = 0; v < S::kCh / 2; ++v) {
+        if ((DT == DT_I8 ? 2 * v : v) >= steps) break;
         uint32_t v4[4];
         ldmatrix4<true>(v4, st + kTok * S::kRowB + f_at + (f_ch ^ (v << 5)));
         if constexpr (DT == DT_I8) {
@@ -622,6 +634,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
             const uint32_t a2 = codes_f16<0x4240>(y), a3 = codes_f16<0x4341>(y);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+              if (2 * v + i >= steps) continue;
               float (&acc)[4] = o[2 * v + i][nt];
               mma16816<DT>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
               mma16816<DT>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
@@ -683,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, Shape<VC, NT, DT>::kMinCtas)
         // a warp without a live token has weight 0 (and the sum 0)
         const float f = mst[w][j][0] == -INFINITY ? 0.0f : ex2(mst[w][j][0] - M);
         const float4 x = *reinterpret_cast<const float4*>(
-            reinterpret_cast<const float*>(smem + w * S::kRingB) + j * S::kOStride + d);
+            reinterpret_cast<const float*>(smem + w * p.ring) + j * S::kOStride + d);
         acc.x = fmaf(f, x.x, acc.x);
         acc.y = fmaf(f, x.y, acc.y);
         acc.z = fmaf(f, x.z, acc.z);
@@ -1056,23 +1069,25 @@ int log2_of(int x) {
 // accumulators of 16 heads still fit.
 int heads_per_chunk(int group, int D) { return group > 8 && D <= 128 ? 16 : 8; }
 
-// Up to here a unit is one CTA's (one launch, no join).  32 units of 256-byte rows: 512 tokens 8.7 us against 9.4 of
-// the split, 768 tokens 11.3 against 9.6; 128 units: 10.2 against 14.5 and 13.8 against 18.4.
-constexpr int kDirect = 512;
+// Up to so many tokens (more with more units, which share the GPU) a unit is one CTA's: one launch and no join.
+// 256-byte rows, direct against split: 4 units of 512 tokens 7.7 us against 8.0, of 768 tokens 9.7 against 8.4;
+// 32 units of 768 tokens 9.9 against 9.7; 128 units of 1024 tokens 15.2 against 22.0, of 2048 24.9 against 32.3;
+// 256 units of 1024 tokens 25.4 against 30.9.  Equal lengths; where they differ the split gains.
+constexpr int kDirect = 512, kDirectPer = 24, kDirectMost = 2048;
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Plan {
   int hp, nch, units, hs, vc, nt, grid, resident, unit_blocks;
-  bool direct;
+  bool direct, wide;
   int64_t blocks;
   size_t off_stats, off_part, off_scores, bytes;
 };
 
 template <int VC, int NT>
 int min_ctas(int dt) {
-  return dt == DT_BF16 ? Shape<VC, NT, DT_BF16>::kMinCtas
-                       : (dt == DT_F16 ? Shape<VC, NT, DT_F16>::kMinCtas : Shape<VC, NT, DT_I8>::kMinCtas);
+  return dt == DT_BF16 ? Shape<VC, NT, DT_BF16, kWarps>::kMinCtas
+                       : (dt == DT_F16 ? Shape<VC, NT, DT_F16, kWarps>::kMinCtas : Shape<VC, NT, DT_I8, kWarps>::kMinCtas);
 }
 
 int ctas_per_sm(int vc, int nt, int dt) {
@@ -1100,7 +1115,11 @@ Plan make_plan(int batch, int n_kv, int n_heads, int D, int dtype, int max_len, 
   r.resident = num_sms * ctas_per_sm(r.vc, r.nt, dt);
   r.grid = (int)working_ctas(r.blocks, r.resident);
   r.unit_blocks = (max_len + kTok - 1) / kTok;
-  r.direct = max_len <= kDirect && (!accumulate || r.nch == 1);
+  r.direct = max_len <= std::max(kDirect, std::min(kDirectMost, kDirectPer * r.units)) && (!accumulate || r.nch == 1);
+  // Eight warps a CTA where every CTA has an SM to itself (128 units of 1024 tokens: 15.2 us against 20.0; 256
+  // units: 28.5 against 25.4), if there are blocks for them.
+  r.wide = r.direct && r.units <= num_sms && r.unit_blocks > kWarps &&
+           2 * kTok * (r.vc * 64 * (dt == DT_I8 ? 1 : 2)) <= kWideStage;
   if (r.direct) {
     r.grid = r.units;
     r.off_stats = r.off_part = r.off_scores = 0;
@@ -1115,28 +1134,43 @@ Plan make_plan(int batch, int n_kv, int n_heads, int D, int dtype, int max_len, 
   return r;
 }
 
-// Raises a kernel's dynamic shared memory limit once per device.
-template <int VC, int NT, int DT>
-cudaError_t launch_one(int grid, const PagedParams& p, cudaStream_t stream) {
-  using S = Shape<VC, NT, DT>;
-  static std::atomic<uint64_t> ready{0};  // devices (bit = number mod 64)
+// `blocks`: at most so many for a warp.  Raises the kernel's dynamic shared memory limit once per device.
+template <int VC, int NT, int DT, int W, bool FULL>
+cudaError_t launch_one(int grid, int blocks, PagedParams p, cudaStream_t stream) {
+  using S = Shape<VC, NT, DT, W>;
+  static std::atomic<uint64_t> ready{0};  // devices (bit = number)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(paged_decode_kernel<VC, NT, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(paged_decode_kernel<VC, NT, DT, W, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::smem(S::kStages));
     if (e != cudaSuccess) return e;
-    ready.fetch_or(bit, std::memory_order_relaxed);
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  return lk::launch_pdl(paged_decode_kernel<VC, NT, DT>, dim3(grid), dim3(kThreads), stream, p, S::kSmem);
+  p.ring = S::ring(blocks);
+  return lk::launch_pdl(paged_decode_kernel<VC, NT, DT, W, FULL>, dim3(grid), dim3(W * 32), stream, p, S::smem(blocks));
+}
+
+template <int VC, int NT, int DT, int W>
+cudaError_t launch_dim(int grid, int blocks, const PagedParams& p, cudaStream_t stream) {
+  return p.D == VC * 64 ? launch_one<VC, NT, DT, W, true>(grid, blocks, p, stream)
+                        : launch_one<VC, NT, DT, W, false>(grid, blocks, p, stream);
+}
+
+template <int VC, int NT, int DT>
+cudaError_t launch_warps(const Plan& r, const PagedParams& p, cudaStream_t stream) {
+  if constexpr (Shape<VC, NT, DT, 8>::kStageB <= kWideStage) {
+    if (r.wide) return launch_dim<VC, NT, DT, 8>(r.grid, (r.unit_blocks + 7) / 8, p, stream);
+  }
+  return launch_dim<VC, NT, DT, kWarps>(r.grid, r.direct ? (r.unit_blocks + kWarps - 1) / kWarps : 1 << 20, p, stream);
 }
 
 template <int VC, int NT>
-cudaError_t launch_split(int dt, int grid, const PagedParams& p, cudaStream_t stream) {
-  if (dt == DT_BF16) return launch_one<VC, NT, DT_BF16>(grid, p, stream);
-  if (dt == DT_F16) return launch_one<VC, NT, DT_F16>(grid, p, stream);
-  return launch_one<VC, NT, DT_I8>(grid, p, stream);
+cudaError_t launch_split(int dt, const Plan& r, const PagedParams& p, cudaStream_t stream) {
+  if (dt == DT_BF16) return launch_warps<VC, NT, DT_BF16>(r, p, stream);
+  if (dt == DT_F16) return launch_warps<VC, NT, DT_F16>(r, p, stream);
+  return launch_warps<VC, NT, DT_I8>(r, p, stream);
 }
 
 }  // namespace
@@ -1194,12 +1228,12 @@ cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream)
   p.offset = dt == DT_BF16 ? 0.0f : kHeld;
   cudaError_t e;
   switch (r.vc * 2 + (r.nt - 1)) {
-    case 2: e = launch_split<1, 1>(dt, r.grid, p, stream); break;
-    case 3: e = launch_split<1, 2>(dt, r.grid, p, stream); break;
-    case 4: e = launch_split<2, 1>(dt, r.grid, p, stream); break;
-    case 5: e = launch_split<2, 2>(dt, r.grid, p, stream); break;
-    case 6: e = launch_split<3, 1>(dt, r.grid, p, stream); break;
-    default: e = launch_split<4, 1>(dt, r.grid, p, stream); break;
+    case 2: e = launch_split<1, 1>(dt, r, p, stream); break;
+    case 3: e = launch_split<1, 2>(dt, r, p, stream); break;
+    case 4: e = launch_split<2, 1>(dt, r, p, stream); break;
+    case 5: e = launch_split<2, 2>(dt, r, p, stream); break;
+    case 6: e = launch_split<3, 1>(dt, r, p, stream); break;
+    default: e = launch_split<4, 1>(dt, r, p, stream); break;
   }
   if (e != cudaSuccess || r.direct) return e;
   JoinParams j{};

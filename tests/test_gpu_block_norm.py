@@ -69,7 +69,8 @@ def run(m, width, dt, post, gate, pre, seed=0, eps=EPS, scale=0.5, offset=0):
 
 @pytest.mark.parametrize("dt", [BF, HF, F32])
 @pytest.mark.parametrize("m,width", [(1, 1), (2, 7), (3, 8), (1, 64), (5, 100), (33, 1000), (4, 4096), (2, 5003),
-                                     (3, 8192), (2, 20000), (1, 32768), (2, 32767)])
+                                     (3, 8192), (2, 20000), (1, 32768), (2, 32767),
+                                     (9, 2049), (5, 2062), (300, 4127), (1100, 1001), (260, 6631)])
 def test_all_parts(dt, m, width):
     run(m, width, dt, True, "channel", True, seed=width)
 
