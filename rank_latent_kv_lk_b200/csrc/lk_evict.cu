@@ -94,7 +94,9 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint32_t smem_keys[];  // keys, then a bit a slot: kept
-  __shared__ __align__(16) int hist[3][kBins];
+  // the first pass of long sequences counts in four, one for every fourth lane: weights crowd in few of its bins
+  constexpr int kCopies = kThreads == 1024 ? 4 : 1, kHists = kCopies == 4 ? 4 : 3;
+  __shared__ __align__(16) int hist[kHists][kBins];
   __shared__ int slots[7][kWarps];
   __shared__ int pick[3][3];
   const int unit = blockIdx.x;
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   uint32_t* kept = keys + p.seg_max;
 
   // ---- keys; which tokens are protected stays in `safe` (four bits a turn) for 16 turns, and is read again behind
-  for (int i = tid; i < 3 * kBins / 4; i += kThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  for (int i = tid; i < kHists * kBins / 4; i += kThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
   uint64_t safe = 0;
   int prot = 0;
 #pragma unroll 2
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t d = k[e] - lo;  // keys below lo wrap around to at least 2^bits
-        if (t + e < n && (pass == 0 || (d >> bits) == 0)) atomicAdd(&hist[pass][d >> shift], 1);
+        if (t + e < n && (pass == 0 || (d >> bits) == 0)) atomicAdd(&hist[pass == 0 ? lane & (kCopies - 1) : pass][d >> shift], 1);
       }
     }
     __syncthreads();
@@ -217,7 +219,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     const int top = kBins - kPer * (tid + 1);
     int bin[kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) bin[e] = hist[pass][top + e];
+    for (int e = 0; e < kPer; ++e) {
+      bin[e] = hist[pass][top + e];
+      if constexpr (kCopies == 4) if (pass == 0) {  // and made ready for the next passes
+        bin[e] += hist[1][top + e] + hist[2][top + e] + hist[kHists - 1][top + e];
+        hist[1][top + e] = hist[2][top + e] = 0;
+      }
+    }
     int mine = 0;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) mine += bin[e];
@@ -273,16 +281,17 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   int n_holes;
   int hole = warp_prefix<kWarps>(holes, slots[5], n_holes);
   int mover = warp_prefix<kWarps>(movers, slots[6], all);
-  int32_t* src = p.src + (int64_t)unit * p.cap;
-  int32_t* dst = p.dst + (int64_t)unit * p.cap;
+  // the lists of slots take the keys' place: as many of each, together at most n
+  uint32_t* hole_slot = keys;
+  uint32_t* mover_slot = keys + n_holes;
   for (int w = w0; w < w1; ++w) {
     const uint32_t k = kept[w];
     const int t = 32 * w + lane;
     const int in_budget = min(32, max(0, p.budget - 32 * w));
     const uint32_t low = in_budget == 32 ? 0xffffffffu : (1u << in_budget) - 1;
     const uint32_t hb = ~k & low, mb = k & ~low;
-    if (hb >> lane & 1) dst[hole + __popc(hb & below)] = t;
-    if (mb >> lane & 1) src[mover + __popc(mb & below)] = t;
+    if (hb >> lane & 1) hole_slot[hole + __popc(hb & below)] = t;
+    if (mb >> lane & 1) mover_slot[mover + __popc(mb & below)] = t;
     hole += __popc(hb);
     mover += __popc(mb);
   }
@@ -309,9 +318,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     }
   }
   // ---- the moves: slots become rows, and their mass and positions go along
+  int32_t* src = p.src + (int64_t)unit * p.cap;
+  int32_t* dst = p.dst + (int64_t)unit * p.cap;
+#pragma unroll 4
   for (int j = tid; j < n_holes; j += kThreads) {
-    int d = row_of(__ldcg(dst + j));
-    const int f = row_of(__ldcg(src + j));
+    int d = row_of((int)hole_slot[j]);
+    const int f = row_of((int)mover_slot[j]);
     if (f < 0) d = -1;
     dst[j] = d;
     src[j] = f;
@@ -390,7 +402,7 @@ int move_cap(int max_len, int budget) { return std::max(0, std::min(budget, max_
 
 template <int THREADS>
 cudaError_t launch_select(int units, size_t smem, const EvictParams& p, cudaStream_t stream) {
-  if (smem > 20 * 1024) {  // with the 25 KB of bins beyond the default limit
+  if (smem > 14 * 1024) {  // with the 33 KB of bins beyond the default limit
     const cudaError_t e = cudaFuncSetAttribute(select_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSmemKeys / 32 * 33 * 4);
     if (e != cudaSuccess) return e;
