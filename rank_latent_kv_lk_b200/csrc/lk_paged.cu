@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
   __shared__ float mst[kWarps][S::kHP][2];
   __shared__ float unit_st[S::kHP][2];
   __shared__ float qf[S::kHP];
-  __shared__ int sh[4];  // sequence, its first block, blocks in all, blocks of this sequence
+  __shared__ int sh[4];  // sequence, its first block, blocks in all, length of this sequence
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gid = lane >> 2, tig = lane & 3;
@@ -254,19 +254,23 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
 
   // blocks in all, then this CTA's range and the sequence it starts in
   int64_t i0, i1;
-  int b, b_start, nb;
+  int b, b_start, nb, len;
   if (p.direct) {
     b = blockIdx.x / per_seq;
     b_start = 0;
-    nb = seq_blocks(p, b);
+    len = max(0, min(__ldcg(p.seq_len + b), p.max_len));
+    nb = (len + kTok - 1) / kTok;
     const int hc = blockIdx.x - b * per_seq;
     i0 = (int64_t)hc * nb;
     i1 = i0 + nb;
     if (nb == 0 && hc == 0) zero_rows(p, b, threadIdx.x, kThreads);
   } else {
     if (warp == 0) {
-      int tot = 0;
-      for (int e = lane; e < p.batch; e += 32) tot += seq_blocks(p, e);
+      // (the lengths of the first 32 sequences are read once: a second look is 0.3 us before the first load)
+      const int len0 = lane < p.batch ? max(0, min(__ldcg(p.seq_len + lane), p.max_len)) : 0;
+      const int n0 = (len0 + kTok - 1) / kTok;
+      int tot = n0;
+      for (int e = lane + 32; e < p.batch; e += 32) tot += seq_blocks(p, e);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
       const int64_t N = (int64_t)tot * per_seq;
@@ -276,7 +280,8 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
       __syncwarp();
       for (int e0 = 0; e0 < p.batch; e0 += 32) {
         const int e = e0 + lane;
-        const int n = e < p.batch ? seq_blocks(p, e) : 0;
+        const int l = e0 == 0 ? len0 : (e < p.batch ? max(0, min(__ldcg(p.seq_len + e), p.max_len)) : 0);
+        const int n = (l + kTok - 1) / kTok;
         int inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
         if (n > 0 && first >= (int64_t)at * per_seq && first < (int64_t)(at + n) * per_seq) {
           sh[0] = e;
           sh[1] = at;
-          sh[3] = n;
+          sh[3] = l;
         }
         run += __shfl_sync(0xffffffffu, inc, 31);
       }
@@ -305,13 +310,15 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
     i1 = quotient((blockIdx.x + 1) * N, G);
     b = sh[0];
     b_start = sh[1];
-    nb = sh[3];
+    len = sh[3];
+    nb = (len + kTok - 1) / kTok;
   }
 
   while (i0 < i1) {
     while (i0 >= (int64_t)(b_start + nb) * per_seq) {  // next sequence with tokens
       b_start += nb;
-      nb = seq_blocks(p, ++b);
+      len = max(0, min(__ldcg(p.seq_len + ++b), p.max_len));
+      nb = (len + kTok - 1) / kTok;
     }
     const int in_seq = (int)(i0 - (int64_t)b_start * per_seq);
     const int hc = in_seq / nb, s0 = in_seq - hc * nb;
@@ -319,7 +326,6 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
     const int h = hc / p.nch, n0 = (hc - h * p.nch) * S::kHP;
     const int heads = min(p.group - n0, S::kHP);
     const int unit = b * per_seq + hc;
-    const int len = max(0, min(__ldcg(p.seq_len + b), p.max_len));
     const int32_t* trow = p.table + (int64_t)b * p.width;
 
     // ---- page and row look-ups: lane l holds token l % 16 of a block
