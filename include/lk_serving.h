@@ -34,8 +34,8 @@ extern "C" {
  *
  * A page table, int32 [batch, table_width] on the device, lists each
  * sequence's pages: slot t of sequence b is row t % page_size of page
- * page_table[b * table_width + t / page_size].  Entries behind a sequence's
- * last page are not read.  A page may be listed by several sequences for
+ * page_table[b * table_width + t / page_size]; table_width * page_size is at
+ * most 2^30.  Entries behind a sequence's last page are not read.  A page may be listed by several sequences for
  * reading; a page that is written (append, mass, eviction) must belong to one
  * sequence.  The host cannot check page ids: a kernel that meets one outside
  * [0, n_pages) skips its slots (not attended, written or moved) and
@@ -92,7 +92,8 @@ lk_status lk_paged_append(const lk_paged_cache* cache, const int32_t* page_table
  * workspace: lk_paged_decode_workspace_bytes(...) bytes, 256-byte aligned,
  *   any contents; calls that may run at the same time need their own.
  * Scores, softmax statistics and the output sum are fp32; the weights p meet
- *   V as a sum of two 16-bit terms (relative rounding at most 2^-16).
+ *   V as a sum of two 16-bit terms (relative rounding at most 2^-16; for fp16
+ *   and int8 caches not below 2^-35 of their sum).
  *   Results do not depend on timing.  One launch for a max_seq_len of up to
  *   512 (for accumulate: and a group of at most 8 heads, 16 up to head_dim
  *   128), else two.

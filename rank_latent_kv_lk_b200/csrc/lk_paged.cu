@@ -211,12 +211,18 @@ struct Shape {
   // Stages and CTAs an SM.  Rows of 256 bytes, one sequence of 4224 tokens: 2 stages and 3 CTAs 20.5 us, 3 and 2
   // 22.1, 4 and 1 24.9; rows of 128 bytes, fp16 with weights: 2 and 5 29.1 us, 3 and 4 29.2, 4 and 3 30.2.
   static constexpr int kStages = kStageB <= 2200 ? 4 : (kStageB <= 12288 ? 2 : 3);
-  static constexpr int kMinCtas =
-      W > kWarps ? 1 : (kStageB <= 2200 ? 4 : kStageB <= 4300 ? (NT == 1 ? 5 : 3) : (kStageB <= 9000 ? 3 : (kStageB <= 12288 ? 2 : 1)));
+  static constexpr int kMinCtas = W > kWarps          ? 1
+                                  : kStageB <= 2200  ? 4
+                                  : kStageB <= 4300  ? (NT == 1 ? 5 : 3)
+                                  : kStageB <= 9000  ? 3
+                                  : kStageB <= 12288 ? 2
+                                                     : 1;
   static constexpr int kQB = NT * (kSteps / 2) * 32 * 16;
   static constexpr int kPartialB = kHP * kOStride * 4;
   // A warp's ring: no more stages than it has blocks, and room for its partial.
-  static int ring(int blocks) { return std::max(std::min(kStages, std::max(blocks, 1)) * kStageB, (kPartialB + 127) / 128 * 128); }
+  static int ring(int blocks) {
+    return std::max(std::min(kStages, std::max(blocks, 1)) * kStageB, (kPartialB + 127) / 128 * 128);
+  }
   static int smem(int blocks) { return W * ring(blocks) + kQB; }
   static_assert(kStages <= 4, "live masks of the stages fit in 64 bits");
 };
@@ -460,7 +466,8 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
     const uint32_t f_at = f_row * S::kRowB;
     const uint32_t f_ch = ((lane >> 4) ^ swizzle<S::kCh>(f_row)) << 4;
     // the block's scores of heads 2 tig, tokens gid
-    const int64_t first_block = p.direct ? (int64_t)unit * p.unit_blocks : (int64_t)b_start * per_seq + (int64_t)hc * nb;
+    const int64_t first_block =
+        p.direct ? (int64_t)unit * p.unit_blocks : (int64_t)b_start * per_seq + (int64_t)hc * nb;
     float* sp = p.scores + ((first_block + blk) * p.hs + 2 * tig) * kTok + gid;
     for (; blk < s1; blk += kWarps, sp += kWarps * p.hs * kTok) {
       // ---- request the block S::kStages - 1 ahead, then wait for this one
@@ -1129,7 +1136,7 @@ Plan make_plan(int batch, int n_kv, int n_heads, int D, int dtype, int max_len, 
   if (r.direct) {
     r.grid = r.units;
     r.off_stats = r.off_part = r.off_scores = 0;
-    r.bytes = accumulate ? (size_t)r.blocks * r.hs * kTok * 4 : 1;
+    r.bytes = std::max<size_t>(accumulate ? (size_t)r.blocks * r.hs * kTok * 4 : 0, 256);
     return r;
   }
   const size_t slots = (size_t)r.grid + r.units;

@@ -57,6 +57,8 @@ lk_status check_paged(const lk_paged_cache* c, int32_t batch, int32_t table_widt
   if ((int64_t)c->n_pages * c->n_kv_heads * c->page_size >= (int64_t)1 << 31)
     return fail(LK_ERR_SHAPE, "n_pages * n_kv_heads * page_size must stay below 2^31");
   if (batch < 1 || table_width < 1) return fail(LK_ERR_SHAPE, "batch %d or table_width %d < 1", batch, table_width);
+  if ((int64_t)table_width * c->page_size > (int64_t)1 << 30)
+    return fail(LK_ERR_SHAPE, "table_width * page_size must be at most 2^30");
   if ((int64_t)batch * LK_MAX_HEADS >= (int64_t)1 << 31) return fail(LK_ERR_SHAPE, "batch %d too large", batch);
   return LK_OK;
 }

@@ -95,6 +95,7 @@ def test_decode_refusals(L):
     assert decode(L, batch=0) == E.LK_ERR_SHAPE
     assert decode(L, width=0) == E.LK_ERR_SHAPE
     assert decode(L, max_len=65) == E.LK_ERR_SHAPE            # beyond the table
+    assert decode(L, width=(1 << 26) + 1) == E.LK_ERR_SHAPE   # slots beyond 2^30
     assert decode(L, max_len=-1) == E.LK_ERR_SHAPE
     assert decode(L, heads=3) == E.LK_ERR_SHAPE
     assert decode(L, heads=0) == E.LK_ERR_SHAPE
@@ -116,11 +117,11 @@ def test_decode_refusals(L):
     need = L.lib.lk_paged_decode_workspace_bytes(C.byref(desc(L)), 2, 4, 40, 0)
     assert need > 0 and decode(L, ws_bytes=need - 1) == E.LK_ERR_WORKSPACE
     m = desc(L, mass=at(2), pos=at(3))
-    for n in (40, 4000):                                      # one launch, two launches
+    for n in (0, 40, 4000):                                   # one launch, two launches
         less = L.lib.lk_paged_decode_workspace_bytes(C.byref(m), 2, 4, n, 0)
         more = L.lib.lk_paged_decode_workspace_bytes(C.byref(m), 2, 4, n, 1)
         scores = 2 * 2 * -(-n // 16) * 2 * 16 * 4             # blocks of 16 tokens, 2 heads a group
-        assert more in (scores, less + scores)
+        assert less > 0 and more in (max(scores, 256), less + scores)
 
 
 def test_append_refusals(L):

@@ -44,6 +44,12 @@ CASES = [
     ([2049, 700, 1333], 3, 2, 128, 32, BF, BF),
     ([5000], 1, 1, 128, 16, BF, BF),
     ([0, 0], 2, 2, 64, 16, BF, BF),
+    ([700, 0, 30, 655], 2, 2, 64, 16, BF, BF),          # longer than one CTA a unit takes, an empty one among them
+    ([900, 1000], 2, 10, 96, 32, HF, HF),
+    ([1500, 1, 0, 1499], 16, 2, 48, 8, HF, HF),
+    ([600], 2, 9, 208, 16, BF, BF),
+    ([520] * 40, 1, 1, 32, 128, HF, HF),
+    ([530] * 5 + [0], 33, 1, 16, 16, I8, BF),
     (LENS, 2, 4, 128, 16, I8, BF),
     (LENS, 2, 4, 128, 16, I8, HF),
     (LENS, 1, 1, 16, 2, I8, BF),
