@@ -35,9 +35,9 @@ extern "C" {
  * A page table, int32 [batch, table_width] on the device, lists each
  * sequence's pages: slot t of sequence b is row t % page_size of page
  * page_table[b * table_width + t / page_size]; table_width * page_size is at
- * most 2^30.  Entries behind a sequence's last page are not read.  A page may be listed by several sequences for
- * reading; a page that is written (append, mass, eviction) must belong to one
- * sequence.  The host cannot check page ids: a kernel that meets one outside
+ * most 2^30.  Entries behind a sequence's last page are not read.  A page may
+ * be listed by several sequences for reading; a page that is written (append,
+ * mass, eviction) must belong to one sequence.  The host cannot check page ids: a kernel that meets one outside
  * [0, n_pages) skips its slots (not attended, written or moved) and
  * lk_device_status() reports LK_ERR_DEVICE.
  */
@@ -83,8 +83,9 @@ lk_status lk_paged_append(const lk_paged_cache* cache, const int32_t* page_table
  *   softmax_scale * q[b, j] . k_t.
  * q: LK_BF16 or LK_F16 (the cache's dtype; either for an int8 cache), row
  *   (b, j) at element b * q_stride + j * head_dim; q_stride a multiple of 8.
- * out: [batch, n_heads, head_dim] LK_BF16, LK_F16 or LK_F32.  A sequence of
- *   length 0, and a head whose every score is -infinity, gives zeros.
+ * out: [batch, n_heads, head_dim] LK_BF16, LK_F16 or LK_F32, not over q.  A
+ *   sequence of length 0, and a head whose every score is -infinity, gives
+ *   zeros.
  * seq_len: device int32 [batch], clamped to [0, max_seq_len]; max_seq_len:
  *   host bound, at most table_width * page_size.
  * accumulate != 0 (the cache must have mass): mass of slot t of kv head h
@@ -120,10 +121,12 @@ size_t lk_paged_decode_workspace_bytes(const lk_paged_cache* cache, int32_t batc
  *   sequence (all of a short one) are written there.  Either both are the
  *   cache's own arrays or neither is.  seq_len_out[b] = min(seq_len[b],
  *   budget) (may be seq_len itself).
- * The sequences must not share pages.  budget >= 1; window, n_sink >= 0.
+ * Lengths are clamped to [0, max_seq_len] first.  The sequences must not share
+ * pages.  budget >= 1; window, n_sink >= 0.
  * workspace: lk_paged_evict_workspace_bytes(...) bytes, 256-byte aligned, any
  *   contents; calls that may run at the same time need their own.
- * Two launches.
+ * Two launches, or one where few rows can move (min(budget, max_seq_len -
+ * budget) up to 256) and seq_len_out is not seq_len.
  */
 lk_status lk_paged_evict(const lk_paged_cache* cache, const int32_t* page_table, int32_t batch,
                          int32_t table_width, const int32_t* seq_len, const int32_t* next_pos,

@@ -20,7 +20,8 @@
 // shared memory took 98 us for 16384 tokens a unit against 36 us (every CTA
 // reads every other's bins three times).
 // move_kernel: the listed rows of K and V (and int8 scales), 16 bytes a lane,
-// and the new lengths (which select_kernel's CTAs still read).
+// and the new lengths (which select_kernel's CTAs still read).  Where few rows
+// can move, select_kernel moves them itself.
 // The holes lie below the budget and the moving rows at or above it, so the
 // moves cannot meet.
 #include "lk_serving.cuh"
@@ -50,6 +51,8 @@ struct EvictParams {
   uint32_t* keys;   // [units][n_keys] where they do not fit in shared memory, else null
   int n_pages, page_shift, n_kv, row_bytes, is_i8, batch, width;
   int max_len, budget, window, n_sink, cap, n_keys, seg_max, in_place, lanes;
+  int fused;          // select_kernel moves the rows too
+  int lengths_apart;  // and writes the lengths (seq_len_out is another array)
 };
 
 // Larger mass, larger key; +0 and -0 alike.
@@ -90,6 +93,58 @@ LK_DEVICE int block_scan(int x, int* slots) {
   return warp_prefix<WARPS>(__shfl_sync(0xffffffffu, inc, 31), slots, all) + inc - x;
 }
 
+LK_DEVICE void new_length(const EvictParams& p, int b) {
+  p.seq_len_out[b] = min(max(0, min(__ldcg(p.seq_len + b), p.max_len)), p.budget);
+}
+
+// Rows of K and V (and scales) of `count` moves, this CTA being `part` of `parts` for the unit.  `lanes` lanes per
+// move (the power of two above its 16-byte pieces, K's then V's; 32 take turns), kAhead moves a thread at a time; the
+// next ones' rows are looked up while these travel.
+LK_DEVICE void move_rows(const EvictParams& p, const int32_t* src, const int32_t* dst, int count, int part, int parts,
+                         int threads) {
+  const int vec = p.row_bytes / 16, pieces = 2 * vec;
+  const int sub = (int)threadIdx.x & (p.lanes - 1), per = threads / p.lanes;
+  const int stride = parts * per * kAhead;
+  int s[kAhead], d[kAhead];
+  auto look_up = [&](int m0) {
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int m = m0 + e * per;
+      s[e] = m < count ? src[m] : -1;
+      d[e] = m < count ? dst[m] : -1;
+    }
+  };
+  int m0 = part * per * kAhead + (int)threadIdx.x / p.lanes;
+  look_up(m0);
+  for (; m0 < count; m0 += stride) {
+    int64_t from[kAhead], to[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const bool in = s[e] >= 0 && d[e] >= 0;
+      from[e] = in ? (int64_t)s[e] * p.row_bytes : -1;
+      to[e] = (int64_t)d[e] * p.row_bytes;
+    }
+    for (int c = sub; c < pieces; c += p.lanes) {
+      uint8_t* base = (c < vec ? p.k : p.v) + 16 * (c < vec ? c : c - vec);
+      uint4 x[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (from[e] >= 0) x[e] = __ldcg(reinterpret_cast<const uint4*>(base + from[e]));
+      if (p.is_i8 && (c == 0 || c == vec)) {
+        float* sc = c < vec ? p.ks : p.vs;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          if (from[e] >= 0) sc[d[e]] = __ldcg(sc + s[e]);
+      }
+      if (c + p.lanes >= pieces) look_up(m0 + stride);
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (from[e] >= 0) *reinterpret_cast<uint4*>(base + to[e]) = x[e];
+    }
+    if (sub >= pieces) look_up(m0 + stride);
+  }
+}
+
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kWarps = kThreads / 32;
@@ -104,6 +159,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   lk_grid_dep_wait();
   lk_grid_dep_launch();
+  if (p.lengths_apart && h == 0 && tid == 0) new_length(p, b);
   const int n = max(0, min(__ldcg(p.seq_len + b), p.max_len));
   const int newest = __ldcg(p.next_pos + b) - p.window;
   const int32_t* trow = p.table + (int64_t)b * p.width;
@@ -325,12 +381,22 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     int d = row_of((int)hole_slot[j]);
     const int f = row_of((int)mover_slot[j]);
     if (f < 0) d = -1;
-    dst[j] = d;
-    src[j] = f;
+    if (p.fused) {
+      hole_slot[j] = (uint32_t)d;
+      mover_slot[j] = (uint32_t)f;
+    } else {
+      dst[j] = d;
+      src[j] = f;
+    }
     if (d >= 0) {
       p.mass_out[d] = __ldcg(p.mass + f);
       p.pos_out[d] = __ldcg(p.pos + f);
     }
+  }
+  if (p.fused) {
+    __syncthreads();
+    move_rows(p, reinterpret_cast<const int32_t*>(mover_slot), reinterpret_cast<const int32_t*>(hole_slot), n_holes, 0,
+              1, kThreads);
   }
 }
 
@@ -338,56 +404,17 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   const int unit = blockIdx.x;
   lk_grid_dep_wait();
   lk_grid_dep_launch();
-  if (blockIdx.y == 0 && unit % p.n_kv == 0 && threadIdx.x == 0) {
-    const int b = unit / p.n_kv;
-    p.seq_len_out[b] = min(max(0, min(__ldcg(p.seq_len + b), p.max_len)), p.budget);
-  }
-  const int count = __ldcg(p.counts + unit);
-  const int32_t* src = p.src + (int64_t)unit * p.cap;
-  const int32_t* dst = p.dst + (int64_t)unit * p.cap;
-  // `lanes` lanes per move (the power of two above its 16-byte pieces, K's then V's; 32 take turns)
-  const int vec = p.row_bytes / 16, pieces = 2 * vec;
-  const int sub = (int)threadIdx.x & (p.lanes - 1), per = kMoveThreads / p.lanes;
-  // kAhead moves a thread at a time; the next ones' rows are looked up while these travel
-  const int stride = gridDim.y * per * kAhead;
-  int s[kAhead], d[kAhead];
-  auto look_up = [&](int m0) {
-#pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      const int m = m0 + e * per;
-      s[e] = m < count ? __ldcg(src + m) : -1;
-      d[e] = m < count ? __ldcg(dst + m) : -1;
-    }
-  };
-  int m0 = blockIdx.y * per * kAhead + (int)threadIdx.x / p.lanes;
-  look_up(m0);
-  for (; m0 < count; m0 += stride) {
-    int64_t from[kAhead], to[kAhead];
-#pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      const bool in = s[e] >= 0 && d[e] >= 0;
-      from[e] = in ? (int64_t)s[e] * p.row_bytes : -1;
-      to[e] = (int64_t)d[e] * p.row_bytes;
-    }
-    for (int c = sub; c < pieces; c += p.lanes) {
-      uint8_t* base = (c < vec ? p.k : p.v) + 16 * (c < vec ? c : c - vec);
-      uint4 x[kAhead];
-#pragma unroll
-      for (int e = 0; e < kAhead; ++e)
-        if (from[e] >= 0) x[e] = __ldcg(reinterpret_cast<const uint4*>(base + from[e]));
-      if (p.is_i8 && (c == 0 || c == vec)) {
-        float* sc = c < vec ? p.ks : p.vs;
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e)
-          if (from[e] >= 0) sc[d[e]] = __ldcg(sc + s[e]);
-      }
-      if (c + p.lanes >= pieces) look_up(m0 + stride);
-#pragma unroll
-      for (int e = 0; e < kAhead; ++e)
-        if (from[e] >= 0) *reinterpret_cast<uint4*>(base + to[e]) = x[e];
-    }
-    if (sub >= pieces) look_up(m0 + stride);
-  }
+  if (blockIdx.y == 0 && unit % p.n_kv == 0 && threadIdx.x == 0) new_length(p, unit / p.n_kv);
+  move_rows(p, p.src + (int64_t)unit * p.cap, p.dst + (int64_t)unit * p.cap, __ldcg(p.counts + unit), blockIdx.y,
+            gridDim.y, kMoveThreads);
+}
+
+// The lengths alone, where the rows are moved already and other CTAs still had the lengths to read.
+__global__ void length_kernel(const __grid_constant__ EvictParams p) {
+  lk_grid_dep_wait();
+  lk_grid_dep_launch();
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b < p.batch) new_length(p, b);
 }
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -454,6 +481,10 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   p.n_sink = a.n_sink;
   p.cap = move_cap(a.max_len, a.budget);
   p.in_place = a.mass_out == c.mass;
+  // Few rows can move: the selecting CTA moves them itself (32 x 8 units, 2112 slots to 2048: 14.7 us
+  // against 18.3).
+  p.fused = p.cap <= 256;
+  p.lengths_apart = p.fused && a.seq_len_out != a.seq_len;
   const size_t lists = round256((size_t)units * p.cap * 4);
   p.counts = reinterpret_cast<int32_t*>(ws);
   p.src = reinterpret_cast<int32_t*>(ws + round256((size_t)units * 4));
@@ -468,7 +499,8 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   if (a.max_len <= 1024) e = launch_select<256>(units, smem, p, stream);
   else if (a.max_len <= 4096) e = launch_select<512>(units, smem, p, stream);
   else e = launch_select<1024>(units, smem, p, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.lengths_apart) return e;
+  if (p.fused) return launch_pdl(length_kernel, dim3((c.batch + 127) / 128), dim3(128), stream, p);
   // CTAs for a unit's most moves, but no more in all than twice what stays resident (dealing all units' moves
   // out in equal ranges needs a prefix sum per CTA, which cost more than ragged batches gain)
   const int rows = kMoveThreads / p.lanes * kAhead;

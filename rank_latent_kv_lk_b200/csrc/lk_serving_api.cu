@@ -27,6 +27,14 @@ lk_status cuda_fail(cudaError_t e, const char* where) {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether two buffers (null: none) share a byte.
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + b_bytes && y < x + a_bytes;
+}
+
+size_t size_of(lk_dtype t) { return t == LK_F32 ? 4 : (t == LK_I8 ? 1 : 2); }
+
 int num_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
@@ -113,6 +121,13 @@ lk_status lk_paged_append(const lk_paged_cache* cache, const int32_t* page_table
   if (token_stride < cache->n_kv_heads * cache->head_dim)
     return fail(LK_ERR_SHAPE, "token_stride %d < n_kv_heads * head_dim", token_stride);
   if (!aligned(k_new, 16) || !aligned(v_new, 16)) return fail(LK_ERR_ALIGN, "k_new and v_new must be 16-byte aligned");
+  const size_t len_b = (size_t)batch * 4;
+  if ((seq_len_out != seq_len && overlap(seq_len_out, len_b, seq_len, len_b)) ||
+      (next_pos_out != next_pos && overlap(next_pos_out, len_b, next_pos, len_b)) ||
+      overlap(seq_len_out, len_b, next_pos, len_b) || overlap(seq_len_out, len_b, next_pos_out, len_b) ||
+      overlap(next_pos_out, len_b, seq_len, len_b) || overlap(seq_len_out, len_b, new_len, len_b) ||
+      overlap(next_pos_out, len_b, new_len, len_b))
+    return fail(LK_ERR_INVALID_ARG, "seq_len_out is seq_len and next_pos_out is next_pos, or they overlap no other");
   if ((cache->mass != nullptr) != (next_pos != nullptr) || (next_pos != nullptr) != (next_pos_out != nullptr))
     return fail(LK_ERR_INVALID_ARG, "next_pos and next_pos_out belong to a cache with mass, and only to it");
   lk::PagedAppendLaunch a{};
@@ -159,6 +174,9 @@ lk_status lk_paged_decode_attn(const lk_paged_cache* cache, const int32_t* page_
   if (q_stride % 8 != 0) return fail(LK_ERR_ALIGN, "q_stride %d must be a multiple of 8", q_stride);
   if (q_stride < n_heads * cache->head_dim) return fail(LK_ERR_SHAPE, "q_stride %d < n_heads * head_dim", q_stride);
   if (!aligned(q, 16) || !aligned(out, 16)) return fail(LK_ERR_ALIGN, "q and out must be 16-byte aligned");
+  if (overlap(q, ((size_t)(batch - 1) * q_stride + (size_t)n_heads * cache->head_dim) * 2, out,
+              (size_t)batch * n_heads * cache->head_dim * size_of(out_dtype)))
+    return fail(LK_ERR_INVALID_ARG, "out must not overlap q");
   if (accumulate != 0 && accumulate != 1) return fail(LK_ERR_INVALID_ARG, "accumulate must be 0 or 1");
   if (accumulate && !cache->mass) return fail(LK_ERR_INVALID_ARG, "accumulate needs a cache with mass");
   if (!(softmax_scale == softmax_scale)) return fail(LK_ERR_INVALID_ARG, "softmax_scale is NaN");
@@ -210,6 +228,16 @@ lk_status lk_paged_evict(const lk_paged_cache* cache, const int32_t* page_table,
     return fail(LK_ERR_INVALID_ARG, "either both or neither of mass_out and pos_out are the cache's own");
   if (!aligned(mass_out, 16) || !aligned(pos_out, 16))
     return fail(LK_ERR_ALIGN, "mass_out and pos_out must be 16-byte aligned");
+  const size_t len_b = (size_t)batch * 4;
+  if ((seq_len_out != seq_len && overlap(seq_len_out, len_b, seq_len, len_b)) ||
+      overlap(seq_len_out, len_b, next_pos, len_b))
+    return fail(LK_ERR_INVALID_ARG, "seq_len_out is seq_len or overlaps neither it nor next_pos");
+  const size_t row_bytes = (size_t)cache->n_pages * cache->n_kv_heads * cache->page_size * 4;
+  if ((mass_out != cache->mass && overlap(mass_out, row_bytes, cache->mass, row_bytes)) ||
+      (pos_out != cache->pos && overlap(pos_out, row_bytes, cache->pos, row_bytes)) ||
+      overlap(mass_out, row_bytes, cache->pos, row_bytes) || overlap(pos_out, row_bytes, cache->mass, row_bytes) ||
+      overlap(mass_out, row_bytes, pos_out, row_bytes))
+    return fail(LK_ERR_INVALID_ARG, "mass_out and pos_out are the cache's own or overlap neither them nor each other");
   const size_t need = lk::paged_evict_workspace_bytes(batch * cache->n_kv_heads, max_seq_len, budget);
   if (!workspace || workspace_bytes < need)
     return fail(LK_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
@@ -285,6 +313,11 @@ lk_status lk_w4_linear(const void* packed, int32_t n_out, int32_t k_in, int32_t 
   if (!aligned(packed, 256)) return fail(LK_ERR_ALIGN, "packed must be 256-byte aligned");
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16))
     return fail(LK_ERR_ALIGN, "x, y and residual must be 16-byte aligned");
+  const size_t y_bytes = (size_t)m * n_out * size_of(y_dtype);
+  if (m > 0 && overlap(x, ((size_t)(m - 1) * x_stride + k_in) * 2, y, y_bytes))
+    return fail(LK_ERR_INVALID_ARG, "y must not overlap x");
+  if (residual != y && overlap(residual, (size_t)m * n_out * 2, y, y_bytes))
+    return fail(LK_ERR_INVALID_ARG, "residual is y or does not overlap it");
   lk::W4Launch a{};
   a.packed = packed;
   a.n_out = n_out;
@@ -318,6 +351,14 @@ lk_status lk_rmsnorm_gate_residual(const void* y, const void* x, const void* w_p
   const size_t es = dtype == LK_F32 ? 4 : 2;
   for (const void* t : {y, x, w_post, gate, w_pre, (const void*)x_out, (const void*)h})
     if (!aligned(t, es)) return fail(LK_ERR_ALIGN, "pointers must be aligned to their elements");
+  const size_t rows_b = (size_t)m * width * es, row_b = (size_t)width * es;
+  for (const void* o : {(const void*)x_out, (const void*)h}) {
+    if ((o != y && overlap(o, rows_b, y, rows_b)) || (o != x && overlap(o, rows_b, x, rows_b)) ||
+        overlap(o, rows_b, w_post, row_b) || overlap(o, rows_b, w_pre, row_b) ||
+        overlap(o, rows_b, gate, gate_per_row ? rows_b : row_b))
+      return fail(LK_ERR_INVALID_ARG, "an output is y or x (h: y) or overlaps no input");
+  }
+  if (overlap(x_out, rows_b, h, rows_b)) return fail(LK_ERR_INVALID_ARG, "x_out and h overlap");
   lk::BlockNormLaunch a{};
   a.y = y;
   a.x = x;

@@ -108,6 +108,8 @@ def test_decode_refusals(L):
     assert decode(L, q_stride=248) == E.LK_ERR_SHAPE
     assert decode(L, q=at(5) + 2) == E.LK_ERR_ALIGN
     assert decode(L, out=at(7) + 8) == E.LK_ERR_ALIGN
+    assert decode(L, out=at(5)) == E.LK_ERR_INVALID_ARG       # over q
+    assert decode(L, out=at(5) + 1008) == E.LK_ERR_INVALID_ARG
     assert decode(L, acc=1) == E.LK_ERR_INVALID_ARG           # a cache without mass
     assert decode(L, acc=2) == E.LK_ERR_INVALID_ARG
     assert decode(L, scale=float("nan")) == E.LK_ERR_INVALID_ARG
@@ -140,6 +142,9 @@ def test_append_refusals(L):
     assert append(L, m) == E.LK_ERR_INVALID_ARG               # mass without positions
     assert append(L, m, nxt=at(9)) == E.LK_ERR_INVALID_ARG
     assert append(L, nxt=at(9), nxt_out=at(9)) == E.LK_ERR_INVALID_ARG
+    assert append(L, seq_out=at(7) + 4) == E.LK_ERR_INVALID_ARG           # lengths shifted by one
+    assert append(L, m, nxt=at(7), nxt_out=at(7)) == E.LK_ERR_INVALID_ARG  # lengths and positions in one array
+    assert append(L, new_len=at(7)) == E.LK_ERR_INVALID_ARG
 
 
 def test_evict_refusals(L):
@@ -153,6 +158,11 @@ def test_evict_refusals(L):
     assert evict(L, max_len=65) == E.LK_ERR_SHAPE
     assert evict(L, mass=at(9)) == E.LK_ERR_INVALID_ARG       # one in place, one not
     assert evict(L, mass=at(9) + 4, pos=at(10)) == E.LK_ERR_ALIGN
+    assert evict(L, mass=at(2) + 64, pos=at(10)) == E.LK_ERR_INVALID_ARG  # partly over the cache's
+    assert evict(L, mass=at(9), pos=at(9) + 512) == E.LK_ERR_INVALID_ARG  # over each other
+    assert evict(L, mass=at(3), pos=at(9)) == E.LK_ERR_INVALID_ARG
+    assert evict(L, seq_out=at(5) + 4) == E.LK_ERR_INVALID_ARG
+    assert evict(L, seq_out=at(6)) == E.LK_ERR_INVALID_ARG    # over the positions
     assert evict(L, ws_bytes=8) == E.LK_ERR_WORKSPACE
     assert evict(L, ws=at(8) + 16) == E.LK_ERR_ALIGN
 
@@ -177,6 +187,8 @@ def test_w4_refusals(L):
     assert w4(L, gated=1, res=at(3)) == E.LK_ERR_UNSUPPORTED
     assert w4(L, gated=2) == E.LK_ERR_INVALID_ARG
     assert w4(L, res=at(2), ydt=L.LK_F32) == E.LK_ERR_INVALID_ARG
+    assert w4(L, res=at(2) + 16) == E.LK_ERR_INVALID_ARG      # partly over y
+    assert w4(L, y=at(1) + 256) == E.LK_ERR_INVALID_ARG       # over x
     assert w4(L, packed=at(0) + 16) == E.LK_ERR_ALIGN
     assert w4(L, x=at(1) + 2) == E.LK_ERR_ALIGN
 
@@ -212,6 +224,10 @@ def test_norm_refusals(L):
     assert norm(h=at(3)) == E.LK_ERR_INVALID_ARG
     assert norm(wq=at(3), h=at(1)) == E.LK_ERR_INVALID_ARG    # h over x
     assert norm(wq=at(3), h=at(2)) == E.LK_ERR_INVALID_ARG    # h over x_out
+    assert norm(xo=at(0) + 2) == E.LK_ERR_INVALID_ARG         # partly over y
+    assert norm(wp=at(2) + 64) == E.LK_ERR_INVALID_ARG        # a weight under an output
+    assert norm(gate=at(2), per_row=1) == E.LK_ERR_INVALID_ARG
+    assert norm(wq=at(3), h=at(2) + 128) == E.LK_ERR_INVALID_ARG
     assert norm(per_row=2) == E.LK_ERR_INVALID_ARG
     assert norm(eps=-1.0) == E.LK_ERR_INVALID_ARG
     assert norm(eps=float("nan")) == E.LK_ERR_INVALID_ARG

@@ -114,6 +114,32 @@ def test_evict_long_sequences(lens, budget):
         assert (got[0][len(src):] == 0).all()
 
 
+@pytest.mark.parametrize("dt", [BF, I8])
+@pytest.mark.parametrize("lens,budget", [([260, 100, 300], 200), ([900, 10], 400)])
+def test_outputs_apart_and_in_place_agree(dt, lens, budget):
+    # the lengths in another array or in place; few rows that move (one launch) and many
+    import rank_latent_kv_lk_b200 as lk
+    got = []
+    for apart in (False, True):
+        pages = Pages(lens, 2, 48, 16, dt, seed=4, mass=True)
+        cache, seq = pages.cuda(), pages.seq()
+        kw = {}
+        if apart:
+            kw = dict(mass_out=torch.full_like(cache.mass, -1), pos_out=torch.full_like(cache.pos, -1),
+                      seq_len_out=torch.full_like(seq, -1))
+        lk.paged_evict(cache, pages.table.cuda(), seq, seq + 2, max(lens), budget, window=5, n_sink=3, **kw)
+        if apart:
+            assert seq.tolist() == lens
+            assert torch.equal(cache.mass.cpu().nan_to_num(9), pages.mass.nan_to_num(9))
+            seq, cache.mass, cache.pos = kw["seq_len_out"], kw["mass_out"], kw["pos_out"]
+        assert seq.tolist() == [min(n, budget) for n in lens]
+        got.append([[pages.rows(t.cpu(), b, h, min(n, budget)) for t in (cache.k, cache.v, cache.mass, cache.pos)]
+                    for b, n in enumerate(lens) for h in range(2)])
+    for a, b in zip(*got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
 def test_evict_skips_and_reports_bad_pages():
     import rank_latent_kv_lk_b200 as lk
     pages = Pages([64, 20], 1, 32, 16, BF, seed=2, mass=True)
