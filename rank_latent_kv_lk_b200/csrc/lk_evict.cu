@@ -11,14 +11,14 @@
 // protected tokens 0xFFFFFFFF, or, when they alone exceed the budget, all
 // others 0).  The budget-th largest key is found by narrowing an interval of
 // keys: 2048 bins over the current interval, then the bin that holds it, so
-// three passes (32 bits = 11 + 11 + 10).  Ties at that key go to the lowest
-// slots: each warp owns consecutive slots, so ballots and prefix sums over the
-// warps give every equal key, every hole and every moving token its number.
-// The CTA also writes the kept mass and positions.  Bound by instructions and
-// latency: hence four tokens an access and no look at ties where there are
-// none.  A cluster of 8 CTAs a unit with the bins summed over distributed
-// shared memory took 98 us for 16384 tokens a unit against 36 us (every CTA
-// reads every other's bins three times).
+// three passes (32 bits = 11 + 11 + 10).  Which slots stay becomes a bit each;
+// a thread then takes a word of 32, and prefix sums over the threads number
+// the equal keys (ties go to the lowest slots), the holes and the moving
+// tokens.  The CTA also writes the kept mass and positions.  Bound by
+// instructions and latency: hence four tokens an access, and no look at ties
+// where there are none.  Clusters did not pay: eight CTAs a unit, their bins
+// summed over distributed shared memory, took 98 us for 16384 tokens a unit
+// where one took 36; a pair gained 3 %.
 // move_kernel: the listed rows of K and V (and int8 scales), 16 bytes a lane,
 // and the new lengths (which select_kernel's CTAs still read).  Where few rows
 // can move, select_kernel moves them itself.
@@ -81,7 +81,7 @@ LK_DEVICE int warp_prefix(int x, int* slots, int& all) {
 
 // Exclusive prefix of one value a thread over the block.
 template <int WARPS>
-LK_DEVICE int block_scan(int x, int* slots) {
+LK_DEVICE int block_scan(int x, int* slots, int* sum = nullptr) {
   const int lane = threadIdx.x & 31;
   int inc = x;
 #pragma unroll
@@ -90,7 +90,9 @@ LK_DEVICE int block_scan(int x, int* slots) {
     if (lane >= o) inc += y;
   }
   int all;
-  return warp_prefix<WARPS>(__shfl_sync(0xffffffffu, inc, 31), slots, all) + inc - x;
+  const int before = warp_prefix<WARPS>(__shfl_sync(0xffffffffu, inc, 31), slots, all);
+  if (sum) *sum = all;
+  return before + inc - x;
 }
 
 LK_DEVICE void new_length(const EvictParams& p, int b) {
@@ -148,7 +150,7 @@ LK_DEVICE void move_rows(const EvictParams& p, const int32_t* src, const int32_t
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kWarps = kThreads / 32;
-  extern __shared__ __align__(16) uint32_t smem_keys[];  // keys, then a bit a slot: kept
+  extern __shared__ __align__(16) uint32_t smem_keys[];  // keys, then two bits a slot: kept, equal
   // the first pass of long sequences counts in four, one for every fourth lane: weights crowd in few of its bins
   constexpr int kCopies = kThreads == 1024 ? 4 : 1, kHists = kCopies == 4 ? 4 : 3;
   __shared__ __align__(16) int hist[kHists][kBins];
@@ -208,26 +210,63 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   }
   uint32_t* keys = p.keys ? p.keys + (int64_t)unit * p.n_keys : smem_keys;
   uint32_t* kept = keys + p.seg_max;
+  uint32_t* ties_at = kept + p.seg_max / 32;
 
   // ---- keys; which tokens are protected stays in `safe` (four bits a turn) for 16 turns, and is read again behind
   for (int i = tid; i < kHists * kBins / 4; i += kThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
   uint64_t safe = 0;
   int prot = 0;
-#pragma unroll 2
-  for (int i = 0; 4 * (i * kThreads + tid) < n; ++i) {
-    const int t = 4 * (i * kThreads + tid);
-    int row[4], ps[4];
-    float m[4];
-    load4(t, n, row, m, ps);
+  auto put_keys = [&](int i, const int (&row)[4], const float (&m)[4], const int (&ps)[4]) {
     uint32_t key[4], bits = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       key[e] = row[e] >= 0 ? mass_key(m[e]) : 1u;
       bits |= (uint32_t)(row[e] >= 0 && is_safe(ps[e])) << e;
     }
-    *reinterpret_cast<uint4*>(keys + t) = make_uint4(key[0], key[1], key[2], key[3]);
+    *reinterpret_cast<uint4*>(keys + 4 * (i * kThreads + tid)) = make_uint4(key[0], key[1], key[2], key[3]);
     prot += __popc(bits);
     if (i < 16) safe |= (uint64_t)bits << (4 * i);
+  };
+  if (quads) {  // the page look-ups of four turns, then their mass and positions, are in flight together
+    constexpr int kTurns = 4;
+    for (int i0 = 0; 4 * (i0 * kThreads + tid) < n; i0 += kTurns) {
+      int first[kTurns];
+      float4 f[kTurns];
+      int4 q[kTurns];
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const int t = 4 * ((i0 + i) * kThreads + tid);
+        first[i] = t < n ? row_of(t) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        q[i] = make_int4(0, 0, 0, 0);
+        if (first[i] >= 0) {
+          f[i] = __ldcg(reinterpret_cast<const float4*>(p.mass + first[i]));
+          q[i] = __ldcg(reinterpret_cast<const int4*>(p.pos + first[i]));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const int t = 4 * ((i0 + i) * kThreads + tid);
+        if (t < n) {
+          int row[4];
+          const float m[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
+          const int ps[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) row[e] = first[i] >= 0 && t + e < n ? first[i] + e : -1;
+          put_keys(i0 + i, row, m, ps);
+        }
+      }
+    }
+  } else {
+    for (int i = 0; 4 * (i * kThreads + tid) < n; ++i) {
+      int row[4], ps[4];
+      float m[4];
+      load4(4 * (i * kThreads + tid), n, row, m, ps);
+      put_keys(i, row, m, ps);
+    }
   }
   int n_prot;
 #pragma unroll
@@ -245,11 +284,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
         for (int e = 0; e < 4; ++e) bits |= (uint32_t)(row[e] >= 0 && is_safe(ps[e])) << e;
       }
+      uint4 k4 = *reinterpret_cast<const uint4*>(keys + t);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if ((bits >> e & 1) && !among) keys[t + e] = 0xFFFFFFFFu;
-        if (!(bits >> e & 1) && among) keys[t + e] = 0u;
+        uint32_t& key = e == 0 ? k4.x : (e == 1 ? k4.y : (e == 2 ? k4.z : k4.w));
+        if ((bits >> e & 1) && !among) key = 0xFFFFFFFFu;
+        if (!(bits >> e & 1) && among) key = 0u;
       }
+      *reinterpret_cast<uint4*>(keys + t) = k4;
     }
   }
 
@@ -304,52 +346,67 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     bits = shift;
   }
 
-  // ---- consecutive slots per warp, 32 at a time
-  const uint32_t below = (1u << lane) - 1;
-  const int words = (n + 31) / 32, per = (words + kWarps - 1) / kWarps;
-  const int w0 = min(words, warp * per), w1 = min(words, w0 + per);
+  // ---- a bit a slot: kept, and where ties are to be told apart, equal.  Four slots a lane; eight lanes make a word.
   const bool ties = need < equal;
-  int seen = 0, holes = 0, movers = 0, all;
-  if (ties) {
-    int eq = 0;
-    for (int w = w0; w < w1; ++w) {
-      const int t = 32 * w + lane;
-      eq += __popc(__ballot_sync(0xffffffffu, t < n && keys[t] == lo));
+  const int words = (n + 31) / 32;
+  for (int t = 4 * tid; t - 4 * lane < n; t += 4 * kThreads) {
+    uint32_t k = 0, q = 0;
+    if (t < n) {
+      const uint4 k4 = *reinterpret_cast<const uint4*>(keys + t);
+      const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        k |= (uint32_t)(t + e < n && (ties ? key[e] > lo : key[e] >= lo)) << e;
+        q |= (uint32_t)(t + e < n && key[e] == lo) << e;
+      }
     }
-    seen = warp_prefix<kWarps>(eq, slots[4], all);
-  }
-  for (int w = w0; w < w1; ++w) {
-    const int t = 32 * w + lane;
-    const uint32_t key = t < n ? keys[t] : 0u;
-    bool keep = t < n && key >= lo;
-    if (ties) {
-      const uint32_t e = __ballot_sync(0xffffffffu, t < n && key == lo);
-      if (key == lo) keep = keep && seen + __popc(e & below) < need;
-      seen += __popc(e);
+    k <<= 4 * (lane & 7);
+    q <<= 4 * (lane & 7);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      k |= __shfl_xor_sync(0xffffffffu, k, o);
+      if (ties) q |= __shfl_xor_sync(0xffffffffu, q, o);
     }
-    const uint32_t k = __ballot_sync(0xffffffffu, keep);
-    const int in_budget = min(32, max(0, p.budget - 32 * w));  // slots of the word below the budget
-    const uint32_t low = in_budget == 32 ? 0xffffffffu : (1u << in_budget) - 1;
-    if (lane == 0) kept[w] = k;
-    holes += __popc(~k & low);  // the budget lies below n: such slots are all live
-    movers += __popc(k & ~low);
+    if ((lane & 7) == 0 && t < n) {
+      kept[t >> 5] = k;
+      if (ties) ties_at[t >> 5] = q;
+    }
   }
-  int n_holes;
-  int hole = warp_prefix<kWarps>(holes, slots[5], n_holes);
-  int mover = warp_prefix<kWarps>(movers, slots[6], all);
-  // the lists of slots take the keys' place: as many of each, together at most n
-  uint32_t* hole_slot = keys;
-  uint32_t* mover_slot = keys + n_holes;
-  for (int w = w0; w < w1; ++w) {
-    const uint32_t k = kept[w];
-    const int t = 32 * w + lane;
+  __syncthreads();
+  // ---- a thread a word: the first `need` of the ties are kept too; holes and moving tokens are counted and listed.
+  // The lists of slots take the keys' place: as many of each, so at most half of all.
+  int n_holes = 0, n_movers = 0, n_seen = 0;
+  auto low_of = [&](int w) {  // slots of the word below the budget (which lies below n: such slots are all live)
     const int in_budget = min(32, max(0, p.budget - 32 * w));
-    const uint32_t low = in_budget == 32 ? 0xffffffffu : (1u << in_budget) - 1;
-    const uint32_t hb = ~k & low, mb = k & ~low;
-    if (hb >> lane & 1) hole_slot[hole + __popc(hb & below)] = t;
-    if (mb >> lane & 1) mover_slot[mover + __popc(mb & below)] = t;
-    hole += __popc(hb);
-    mover += __popc(mb);
+    return in_budget == 32 ? 0xffffffffu : (1u << in_budget) - 1;
+  };
+  if (ties) {
+    for (int w0 = 0; w0 < words; w0 += kThreads) {
+      const int w = w0 + tid;
+      uint32_t q = w < words ? ties_at[w] : 0;
+      int all;
+      int left = need - n_seen - block_scan<kWarps>(__popc(q), slots[4], &all);  // of this word's ties are kept
+      while (q && left < __popc(q)) q &= ~(0x80000000u >> __clz(q));  // the highest go
+      if (w < words && left > 0) kept[w] |= q;
+      n_seen += all;
+      __syncthreads();  // slots are read
+    }
+  }
+  uint32_t* hole_slot = keys;
+  uint32_t* mover_slot = keys + p.seg_max / 2;
+  for (int w0 = 0; w0 < words; w0 += kThreads) {
+    const int w = w0 + tid;
+    const uint32_t k = w < words ? kept[w] : 0, low = w < words ? low_of(w) : 0;
+    uint32_t hb = ~k & low, mb = k & ~low;
+    // both counts in one sum: a round of words holds at most 32 kThreads = 2^15 slots
+    int all;
+    const uint32_t at = (uint32_t)block_scan<kWarps>(__popc(hb) | __popc(mb) << 16, slots[6], &all);
+    int hole = n_holes + (int)(at & 0xFFFFu), mover = n_movers + (int)(at >> 16);
+    n_holes += (int)((uint32_t)all & 0xFFFFu);
+    n_movers += (int)((uint32_t)all >> 16);
+    for (; hb; hb &= hb - 1) hole_slot[hole++] = 32 * w + __ffs(hb) - 1;
+    for (; mb; mb &= mb - 1) mover_slot[mover++] = 32 * w + __ffs(mb) - 1;
+    __syncthreads();  // slots are read
   }
   if (tid == 0) p.counts[unit] = n_holes;
   __syncthreads();  // the lists and `kept` are written
@@ -422,7 +479,7 @@ size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 // Slots a CTA holds keys for in shared memory; longer sequences keep theirs in the workspace.
 constexpr int kSmemKeys = 40 * 1024;
 int seg_of(int max_len) { return (max_len + 127) & ~127; }
-size_t spill_words(int max_len) { return (size_t)seg_of(max_len) / 32 * 33; }  // keys and bits
+size_t spill_words(int max_len) { return (size_t)seg_of(max_len) / 32 * 34; }  // keys and bits
 bool spills(int max_len, int budget) { return max_len > budget && seg_of(max_len) > kSmemKeys; }
 
 int move_cap(int max_len, int budget) { return std::max(0, std::min(budget, max_len - budget)); }
@@ -431,7 +488,7 @@ template <int THREADS>
 cudaError_t launch_select(int units, size_t smem, const EvictParams& p, cudaStream_t stream) {
   if (smem > 14 * 1024) {  // with the 33 KB of bins beyond the default limit
     const cudaError_t e = cudaFuncSetAttribute(select_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kSmemKeys / 32 * 33 * 4);
+                                               kSmemKeys / 32 * 34 * 4);
     if (e != cudaSuccess) return e;
   }
   return lk::launch_pdl(select_kernel<THREADS>, dim3(units), dim3(THREADS), stream, p, smem);
@@ -493,7 +550,7 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   p.keys = spill ? reinterpret_cast<uint32_t*>(ws + round256((size_t)units * 4) + 2 * lists) : nullptr;
   p.n_keys = (int)spill_words(a.max_len);
   p.seg_max = seg_of(a.max_len);
-  const size_t smem = spill || a.max_len <= a.budget ? 0 : (size_t)p.seg_max / 32 * 33 * 4;
+  const size_t smem = spill || a.max_len <= a.budget ? 0 : (size_t)p.seg_max / 32 * 34 * 4;
   cudaError_t e;
   // threads for about four slots each
   if (a.max_len <= 1024) e = launch_select<256>(units, smem, p, stream);
@@ -501,10 +558,10 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   else e = launch_select<1024>(units, smem, p, stream);
   if (e != cudaSuccess || p.lengths_apart) return e;
   if (p.fused) return launch_pdl(length_kernel, dim3((c.batch + 127) / 128), dim3(128), stream, p);
-  // CTAs for a unit's most moves, but no more in all than twice what stays resident (dealing all units' moves
+  // CTAs for a unit's most moves, but no more in all than four times what stays resident (dealing all units' moves
   // out in equal ranges needs a prefix sum per CTA, which cost more than ragged batches gain)
   const int rows = kMoveThreads / p.lanes * kAhead;
-  const int chunks = std::max(1, std::min((p.cap + rows - 1) / rows, 8 * a.num_sms / units));
+  const int chunks = std::max(1, std::min((p.cap + rows - 1) / rows, 16 * a.num_sms / units));
   return launch_pdl(move_kernel, dim3(units, chunks), dim3(kMoveThreads), stream, p);
 }
 

@@ -79,7 +79,8 @@ def test_evict_in_place(case, kind):
     compare(pages, cache, want, lens, budget)
 
 
-@pytest.mark.parametrize("lens,budget", [([70000], 30000), ([60000, 100], 50000), ([30001], 7), ([2000, 100001], 1999)])
+@pytest.mark.parametrize("lens,budget", [([70000], 30000), ([60000, 100], 50000), ([30001], 7), ([2000, 100001], 1999),
+                                         ([66000], 33000)])
 def test_evict_long_sequences(lens, budget):
     # longer than shared memory holds keys for
     import rank_latent_kv_lk_b200 as lk
@@ -93,6 +94,9 @@ def test_evict_long_sequences(lens, budget):
     pos = torch.arange(width * page, dtype=torch.int32).repeat(B).view(shape[:3])
     table = torch.randperm(B * width, generator=g).to(torch.int32).view(B, width)
     pos[table.flatten().long()] = pos.clone()
+    if lens == [66000]:  # the upper half of the slots is wanted: whole rounds of words move
+        wanted = torch.arange(width * page).view(width, page) >= 33000
+        mass[table[0].long(), 0] = torch.where(wanted, 1.0 + mass[table[0].long(), 0], 0.0)
     cache = lk.PagedKVCache.from_tensors(k.cuda(), v.cuda(), None, None, mass.cuda(), pos.cuda())
     seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
     out_m, out_p = torch.zeros_like(cache.mass), torch.zeros_like(cache.pos)
