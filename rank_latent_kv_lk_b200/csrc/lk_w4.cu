@@ -155,6 +155,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
                                    : ring + S::kRec;
   constexpr int kXStep = S::kShared ? S::kXStage : S::kStage;
   // Rows behind the last are never filled: a column of a product is one row, and theirs are not stored.
+  // While the kernel before still runs: the records that the ring will ask for first, into L2 (no value is used, so
+  // that it does not matter who wrote them when).  Rows of 11008: 13.5 us -> 12.5; eight or more records ahead 13.3.
+  if (mine) {
+    const uint8_t* first = p.packed + ((int64_t)tile * p.steps + wk) * S::kRec;
+    for (int i = 0; i < S::kStages - 1 && wk + i * p.kn < p.steps; ++i, first += (int64_t)p.kn * S::kRec)
+      if (lane * 128 < S::kRec) asm volatile("prefetch.global.L2 [%0];" ::"l"(first + lane * 128));
+  }
   lk_grid_dep_wait();
   lk_grid_dep_launch();
 
