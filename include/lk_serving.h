@@ -37,9 +37,10 @@ extern "C" {
  * page_table[b * table_width + t / page_size]; table_width * page_size is at
  * most 2^30.  Entries behind a sequence's last page are not read.  A page may
  * be listed by several sequences for reading; a page that is written (append,
- * mass, eviction) must belong to one sequence.  The host cannot check page ids: a kernel that meets one outside
- * [0, n_pages) skips its slots (not attended, written or moved) and
- * lk_device_status() reports LK_ERR_DEVICE.
+ * mass, eviction) must belong to one sequence and be listed once.  The host
+ * cannot check page ids: a kernel that meets one outside [0, n_pages) skips its
+ * slots (not attended, written or moved) and lk_device_status() reports
+ * LK_ERR_DEVICE.
  */
 typedef struct {
   int32_t n_pages, page_size, n_kv_heads, head_dim;
@@ -95,6 +96,9 @@ lk_status lk_paged_append(const lk_paged_cache* cache, const int32_t* page_table
  * Scores, softmax statistics and the output sum are fp32; the weights p meet
  *   V as a sum of two 16-bit terms (relative rounding at most 2^-16; for fp16
  *   and int8 caches not below 2^-35 of their sum).
+ *   Weights are held at up to 2^4 (fp16 and int8 caches: 2^14), and that times
+ *   seq_len |v| has to stay in fp32's range; an infinity in an attended V row
+ *   makes its dim NaN.
  *   Results do not depend on timing.  One launch for a max_seq_len of up to
  *   512 (for accumulate: and a group of at most 8 heads, 16 up to head_dim
  *   128), else two.

@@ -367,7 +367,8 @@ namespace lk {
 
 cudaError_t launch_block_norm(const BlockNormLaunch& a, cudaStream_t stream) {
   if (a.m == 0) return cudaSuccess;
-  NormParams p{a.y, a.x, a.w_post, a.gate, a.w_pre, a.x_out, a.h, a.width, a.gate_per_row, a.scale, a.eps, 1.0f / (float)a.width};
+  NormParams p{a.y,     a.x,     a.w_post,       a.gate,  a.w_pre, a.x_out,
+               a.h,     a.width, a.gate_per_row, a.scale, a.eps,   1.0f / (float)a.width};
   if (a.dtype == LK_F32) return launch_v<T_F32>(p, a.m, stream);
   if (a.dtype == LK_BF16) return launch_v<T_BF16>(p, a.m, stream);
   return launch_v<T_F16>(p, a.m, stream);

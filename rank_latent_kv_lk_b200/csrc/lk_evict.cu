@@ -18,7 +18,8 @@
 // instructions and latency: hence four tokens an access, and no look at ties
 // where there are none.  Clusters did not pay: eight CTAs a unit, their bins
 // summed over distributed shared memory, took 98 us for 16384 tokens a unit
-// where one took 36; a pair gained 3 %.
+// where one took 36; a pair gained 3 %.  With the moves: 32 x 8 units
+// from 2112 to 2048 slots 14.3 us, 8 x 8 of up to 16384 to 4096 44 us.
 // move_kernel: the listed rows of K and V (and int8 scales), 16 bytes a lane,
 // and the new lengths (which select_kernel's CTAs still read).  Where few rows
 // can move, select_kernel moves them itself.
@@ -308,7 +309,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t d = k[e] - lo;  // keys below lo wrap around to at least 2^bits
-        if (t + e < n && (pass == 0 || (d >> bits) == 0)) atomicAdd(&hist[pass == 0 ? lane & (kCopies - 1) : pass][d >> shift], 1);
+        if (t + e < n && (pass == 0 || (d >> bits) == 0))
+          atomicAdd(&hist[pass == 0 ? lane & (kCopies - 1) : pass][d >> shift], 1);
       }
     }
     __syncthreads();

