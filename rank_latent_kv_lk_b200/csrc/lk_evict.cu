@@ -10,8 +10,9 @@
 // order-preserving 32-bit key in shared memory (NaN 1, below every number;
 // protected tokens 0xFFFFFFFF, or, when they alone exceed the budget, all
 // others 0).  The budget-th largest key is found by narrowing an interval of
-// keys: 2048 bins over the current interval, then the bin that holds it, so
-// three passes (32 bits = 11 + 11 + 10).  Which slots stay becomes a bit each;
+// keys: 2048 bins over the current interval, then the bin that holds it, so at
+// most three passes (32 bits = 11 + 11 + 10), and fewer where a bin stays as a
+// whole.  Which slots stay becomes a bit each;
 // a thread then takes a word of 32, and prefix sums over the threads number
 // the equal keys (ties go to the lowest slots), the holes and the moving
 // tokens.  The CTA also writes the kept mass and positions.  Bound by
@@ -19,7 +20,7 @@
 // where there are none.  Clusters did not pay: eight CTAs a unit, their bins
 // summed over distributed shared memory, took 98 us for 16384 tokens a unit
 // where one took 36; a pair gained 3 %.  With the moves: 32 x 8 units
-// from 2112 to 2048 slots 14.3 us, 8 x 8 of up to 16384 to 4096 44 us.
+// from 2112 to 2048 slots 13.1 us, 8 x 8 of up to 16384 to 4096 42 us.
 // move_kernel: the listed rows of K and V (and int8 scales), 16 bytes a lane,
 // and the new lengths (which select_kernel's CTAs still read).  Where few rows
 // can move, select_kernel moves them itself.
@@ -213,20 +214,18 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   uint32_t* kept = keys + p.seg_max;
   uint32_t* ties_at = kept + p.seg_max / 32;
 
-  // ---- keys; which tokens are protected stays in `safe` (four bits a turn) for 16 turns, and is read again behind
+  // ---- keys, as if fewer tokens than the budget were protected
   for (int i = tid; i < kHists * kBins / 4; i += kThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
-  uint64_t safe = 0;
   int prot = 0;
   auto put_keys = [&](int i, const int (&row)[4], const float (&m)[4], const int (&ps)[4]) {
-    uint32_t key[4], bits = 0;
+    uint32_t key[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      key[e] = row[e] >= 0 ? mass_key(m[e]) : 1u;
-      bits |= (uint32_t)(row[e] >= 0 && is_safe(ps[e])) << e;
+      const bool safe = row[e] >= 0 && is_safe(ps[e]);
+      key[e] = safe ? 0xFFFFFFFFu : (row[e] >= 0 ? mass_key(m[e]) : 1u);
+      prot += safe;
     }
     *reinterpret_cast<uint4*>(keys + 4 * (i * kThreads + tid)) = make_uint4(key[0], key[1], key[2], key[3]);
-    prot += __popc(bits);
-    if (i < 16) safe |= (uint64_t)bits << (4 * i);
   };
   if (quads) {  // the page look-ups of four turns, then their mass and positions, are in flight together
     constexpr int kTurns = 4;
@@ -273,26 +272,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) prot += __shfl_xor_sync(0xffffffffu, prot, o);
   warp_prefix<kWarps>(prot, slots[0], n_prot);
-  const bool among = n_prot >= p.budget;  // select among the protected alone
-  if (n_prot > 0) {
-    for (int i = 0; 4 * (i * kThreads + tid) < n; ++i) {
-      const int t = 4 * (i * kThreads + tid);
-      uint32_t bits = i < 16 ? (uint32_t)(safe >> (4 * i)) & 15u : 0;
-      if (i >= 16) {
-        int row[4], ps[4];
-        float m[4];
-        load4(t, n, row, m, ps);
+  if (n_prot >= p.budget) {  // select among the protected alone: the keys again
+    for (int t = 4 * tid; t < n; t += 4 * kThreads) {
+      int row[4], ps[4];
+      float m[4];
+      uint32_t key[4];
+      load4(t, n, row, m, ps);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) bits |= (uint32_t)(row[e] >= 0 && is_safe(ps[e])) << e;
-      }
-      uint4 k4 = *reinterpret_cast<const uint4*>(keys + t);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t& key = e == 0 ? k4.x : (e == 1 ? k4.y : (e == 2 ? k4.z : k4.w));
-        if ((bits >> e & 1) && !among) key = 0xFFFFFFFFu;
-        if (!(bits >> e & 1) && among) key = 0u;
-      }
-      *reinterpret_cast<uint4*>(keys + t) = k4;
+      for (int e = 0; e < 4; ++e) key[e] = row[e] >= 0 && is_safe(ps[e]) ? mass_key(m[e]) : 0u;
+      *reinterpret_cast<uint4*>(keys + t) = make_uint4(key[0], key[1], key[2], key[3]);
     }
   }
 
@@ -346,6 +334,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     need -= pick[pass][1];
     equal = pick[pass][2];
     bits = shift;
+    if (need == equal) break;  // the bin stays as a whole
   }
 
   // ---- a bit a slot: kept, and where ties are to be told apart, equal.  Four slots a lane; eight lanes make a word.

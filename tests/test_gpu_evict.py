@@ -46,6 +46,8 @@ CASES = [
     ([300], 2, 64, 16, BF, 32, 100, 0),       # more protected than the budget
     ([5000, 4097], 1, 32, 128, BF, 1000, 64, 4),
     ([9000], 1, 16, 16, HF, 4500, 0, 1),
+    ([700], 2, 16, 2, BF, 100, 300, 5),       # the same, pages of two rows
+    ([20000, 70], 1, 16, 64, BF, 5000, 6000, 10),
 ]
 
 
@@ -77,6 +79,28 @@ def test_evict_in_place(case, kind):
     lk.device_status()
     assert seq.tolist() == [min(n, budget) for n in lens]
     compare(pages, cache, want, lens, budget)
+
+
+@pytest.mark.parametrize("budget", [199, 200, 201, 399, 400, 401])
+def test_weights_of_a_few_magnitudes(budget):
+    # the limit lies at or beside the end of a bin of equal leading bits: 200 weights each around 1, 2^-40 and 2^-80
+    import rank_latent_kv_lk_b200 as lk
+    n, page = 600, 16
+    g = torch.Generator().manual_seed(budget)
+    mag = torch.tensor([1.0, 2.0 ** -40, 2.0 ** -80]).repeat_interleave(200)[torch.randperm(n, generator=g)]
+    shape = (-(-n // page), 1, page)
+    mass, pos = torch.zeros(shape), torch.zeros(shape, dtype=torch.int32)
+    mass.view(-1)[:n] = mag * (1 + torch.randint(0, 50, (n,), generator=g) * 2.0 ** -20)
+    pos.view(-1)[:n] = torch.arange(n, dtype=torch.int32)
+    k = torch.randn(shape + (16,), generator=g).to(BF)
+    cache = lk.PagedKVCache.from_tensors(k.cuda(), k.cuda(), None, None, mass.cuda(), pos.cuda())
+    seq = torch.tensor([n], dtype=torch.int32, device="cuda")
+    table = torch.arange(shape[0], dtype=torch.int32, device="cuda")[None]
+    lk.paged_evict(cache, table, seq, seq.clone(), n, budget)
+    src = torch.from_numpy(np.asarray(evict(mass.view(-1)[:n].numpy(), pos.view(-1)[:n].numpy(), n, n, budget, 0, 0)))
+    assert seq.tolist() == [budget]
+    for got, was in ((cache.mass, mass), (cache.pos, pos), (cache.k, k), (cache.v, k)):
+        assert torch.equal(got.cpu().flatten(0, 2)[:budget], was.flatten(0, 2)[src])
 
 
 @pytest.mark.parametrize("lens,budget", [([70000], 30000), ([60000, 100], 50000), ([30001], 7), ([2000, 100001], 1999),
