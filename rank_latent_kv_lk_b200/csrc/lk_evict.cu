@@ -149,8 +149,9 @@ LK_DEVICE void move_rows(const EvictParams& p, const int32_t* src, const int32_t
   }
 }
 
+// (At least 1024 threads an SM: 32 x 8 units of 2112 slots 12.1 us with two CTAs of 512, 18.6 with one.)
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint32_t smem_keys[];  // keys, then two bits a slot: kept, equal
   // the first pass of long sequences counts in four, one for every fourth lane: weights crowd in few of its bins
@@ -161,6 +162,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   const int unit = blockIdx.x;
   const int b = unit / p.n_kv, h = unit - b * p.n_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto clear_bins = [&] {
+    for (int i = tid; i < kHists * kBins / 4; i += kThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+  };
+  clear_bins();
   lk_grid_dep_wait();
   lk_grid_dep_launch();
   if (p.lengths_apart && h == 0 && tid == 0) new_length(p, b);
@@ -214,9 +220,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   uint32_t* kept = keys + p.seg_max;
   uint32_t* ties_at = kept + p.seg_max / 32;
 
-  // ---- keys, as if fewer tokens than the budget were protected
-  for (int i = tid; i < kHists * kBins / 4; i += kThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  // ---- keys, as if fewer tokens than the budget were protected.  With outputs apart, the slots below the budget are
+  // written as they come (as many moving tokens as holes overwrite the evicted ones later): reading them again once
+  // the kept ones are known took 1 us more.
   int prot = 0;
+  auto count_first = [&](uint32_t key) { atomicAdd(&hist[lane & (kCopies - 1)][key >> 21], 1); };
   auto put_keys = [&](int i, const int (&row)[4], const float (&m)[4], const int (&ps)[4]) {
     uint32_t key[4];
 #pragma unroll
@@ -225,7 +233,24 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
       key[e] = safe ? 0xFFFFFFFFu : (row[e] >= 0 ? mass_key(m[e]) : 1u);
       prot += safe;
     }
-    *reinterpret_cast<uint4*>(keys + 4 * (i * kThreads + tid)) = make_uint4(key[0], key[1], key[2], key[3]);
+    const int t = 4 * (i * kThreads + tid);
+    *reinterpret_cast<uint4*>(keys + t) = make_uint4(key[0], key[1], key[2], key[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t + e < n) count_first(key[e]);
+    if (!p.in_place) {
+      if (quads && row[0] >= 0 && t + 4 <= p.budget) {
+        *reinterpret_cast<float4*>(p.mass_out + row[0]) = make_float4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<int4*>(p.pos_out + row[0]) = make_int4(ps[0], ps[1], ps[2], ps[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row[e] >= 0 && t + e < p.budget) {
+            p.mass_out[row[e]] = m[e];
+            p.pos_out[row[e]] = ps[e];
+          }
+      }
+    }
   };
   if (quads) {  // the page look-ups of four turns, then their mass and positions, are in flight together
     constexpr int kTurns = 4;
@@ -272,7 +297,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) prot += __shfl_xor_sync(0xffffffffu, prot, o);
   warp_prefix<kWarps>(prot, slots[0], n_prot);
-  if (n_prot >= p.budget) {  // select among the protected alone: the keys again
+  if (n_prot >= p.budget) {  // select among the protected alone: the keys and the first bins again
+    clear_bins();
     for (int t = 4 * tid; t < n; t += 4 * kThreads) {
       int row[4], ps[4];
       float m[4];
@@ -281,7 +307,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
       for (int e = 0; e < 4; ++e) key[e] = row[e] >= 0 && is_safe(ps[e]) ? mass_key(m[e]) : 0u;
       *reinterpret_cast<uint4*>(keys + t) = make_uint4(key[0], key[1], key[2], key[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t + e < n) count_first(key[e]);
     }
+    __syncthreads();
   }
 
   // ---- the budget-th largest key: `need` of the keys in [lo, lo + 2^bits) are still wanted, `equal` there are
@@ -290,18 +320,19 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    if (pass > 0) {  // (the first bins are counted with the keys)
 #pragma unroll 2
-    for (int t = 4 * tid; t < n; t += 4 * kThreads) {
-      const uint4 k4 = *reinterpret_cast<const uint4*>(keys + t);
-      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+      for (int t = 4 * tid; t < n; t += 4 * kThreads) {
+        const uint4 k4 = *reinterpret_cast<const uint4*>(keys + t);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t d = k[e] - lo;  // keys below lo wrap around to at least 2^bits
-        if (t + e < n && (pass == 0 || (d >> bits) == 0))
-          atomicAdd(&hist[pass == 0 ? lane & (kCopies - 1) : pass][d >> shift], 1);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t d = k[e] - lo;  // keys below lo wrap around to at least 2^bits
+          if (t + e < n && (d >> bits) == 0) atomicAdd(&hist[pass][d >> shift], 1);
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
     // consecutive bins a thread, from the top
     constexpr int kPer = kBins / kThreads;
     const int top = kBins - kPer * (tid + 1);
@@ -400,27 +431,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     __syncthreads();  // slots are read
   }
   if (tid == 0) p.counts[unit] = n_holes;
-  __syncthreads();  // the lists and `kept` are written
-  if (!p.in_place) {
-#pragma unroll 2
-    for (int t = 4 * tid; t < p.budget; t += 4 * kThreads) {
-      const uint32_t k = kept[t >> 5] >> (t & 31) & 15u;
-      int row[4], ps[4];
-      float m[4];
-      load4(t, p.budget, row, m, ps);
-      if (quads && k == 15u && row[0] >= 0 && row[3] >= 0) {
-        *reinterpret_cast<float4*>(p.mass_out + row[0]) = make_float4(m[0], m[1], m[2], m[3]);
-        *reinterpret_cast<int4*>(p.pos_out + row[0]) = make_int4(ps[0], ps[1], ps[2], ps[3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if ((k >> e & 1) && row[e] >= 0) {
-            p.mass_out[row[e]] = m[e];
-            p.pos_out[row[e]] = ps[e];
-          }
-      }
-    }
-  }
+  __syncthreads();  // the lists are written
   // ---- the moves: slots become rows, and their mass and positions go along
   int32_t* src = p.src + (int64_t)unit * p.cap;
   int32_t* dst = p.dst + (int64_t)unit * p.cap;
