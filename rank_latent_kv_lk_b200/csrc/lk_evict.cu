@@ -33,6 +33,7 @@ namespace {
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
 constexpr int kAhead = 4;      // moves a thread has in flight
+constexpr int kMostFused = 256;  // moves of a unit that select_kernel makes itself: no more than its threads
 
 struct EvictParams {
   uint8_t* k;
@@ -433,6 +434,29 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
   if (tid == 0) p.counts[unit] = n_holes;
   __syncthreads();  // the lists are written
   // ---- the moves: slots become rows, and their mass and positions go along
+  if (p.fused) {  // at most kMostFused, one a thread; mass and position travel while K and V do
+    int d = -1, ps = 0;
+    float m = 0.0f;
+    if (tid < n_holes) {
+      d = row_of((int)hole_slot[tid]);
+      const int f = row_of((int)mover_slot[tid]);
+      if (f < 0) d = -1;
+      hole_slot[tid] = (uint32_t)d;
+      mover_slot[tid] = (uint32_t)f;
+      if (d >= 0) {
+        m = __ldcg(p.mass + f);
+        ps = __ldcg(p.pos + f);
+      }
+    }
+    __syncthreads();
+    move_rows(p, reinterpret_cast<const int32_t*>(mover_slot), reinterpret_cast<const int32_t*>(hole_slot), n_holes, 0,
+              1, kThreads);
+    if (d >= 0) {
+      p.mass_out[d] = m;
+      p.pos_out[d] = ps;
+    }
+    return;
+  }
   int32_t* src = p.src + (int64_t)unit * p.cap;
   int32_t* dst = p.dst + (int64_t)unit * p.cap;
 #pragma unroll 4
@@ -440,22 +464,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
     int d = row_of((int)hole_slot[j]);
     const int f = row_of((int)mover_slot[j]);
     if (f < 0) d = -1;
-    if (p.fused) {
-      hole_slot[j] = (uint32_t)d;
-      mover_slot[j] = (uint32_t)f;
-    } else {
-      dst[j] = d;
-      src[j] = f;
-    }
+    dst[j] = d;
+    src[j] = f;
     if (d >= 0) {
       p.mass_out[d] = __ldcg(p.mass + f);
       p.pos_out[d] = __ldcg(p.pos + f);
     }
-  }
-  if (p.fused) {
-    __syncthreads();
-    move_rows(p, reinterpret_cast<const int32_t*>(mover_slot), reinterpret_cast<const int32_t*>(hole_slot), n_holes, 0,
-              1, kThreads);
   }
 }
 
@@ -542,7 +556,7 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   p.in_place = a.mass_out == c.mass;
   // Few rows can move: the selecting CTA moves them itself (32 x 8 units, 2112 slots to 2048: 14.7 us
   // against 18.3).
-  p.fused = p.cap <= 256;
+  p.fused = p.cap <= kMostFused;
   p.lengths_apart = p.fused && a.seq_len_out != a.seq_len;
   const size_t lists = round256((size_t)units * p.cap * 4);
   p.counts = reinterpret_cast<int32_t*>(ws);
