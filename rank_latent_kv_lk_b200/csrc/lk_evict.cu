@@ -11,8 +11,8 @@
 // protected tokens 0xFFFFFFFF, or, when they alone exceed the budget, all
 // others 0).  The budget-th largest key is found by narrowing an interval of
 // keys: 2048 bins over the current interval, then the bin that holds it, so at
-// most three passes (32 bits = 11 + 11 + 10), and fewer where a bin stays as a
-// whole.  Which slots stay becomes a bit each;
+// most three passes (32 bits = 11 + 11 + 10), and fewer where a bin stays as
+// a whole; the first bins are counted as the keys are made.  Which slots stay becomes a bit each;
 // a thread then takes a word of 32, and prefix sums over the threads number
 // the equal keys (ties go to the lowest slots), the holes and the moving
 // tokens.  The CTA also writes the kept mass and positions.  Bound by
@@ -20,7 +20,8 @@
 // where there are none.  Clusters did not pay: eight CTAs a unit, their bins
 // summed over distributed shared memory, took 98 us for 16384 tokens a unit
 // where one took 36; a pair gained 3 %.  With the moves: 32 x 8 units
-// from 2112 to 2048 slots 13.1 us, 8 x 8 of up to 16384 to 4096 42 us.
+// from 2112 to 2048 slots 10.9 us, 8 x 8 of up to 16384 to 4096 40.1 us (20 of
+// them the rows' bytes both ways, near the copy bandwidth).
 // move_kernel: the listed rows of K and V (and int8 scales), 16 bytes a lane,
 // and the new lengths (which select_kernel's CTAs still read).  Where few rows
 // can move, select_kernel moves them itself.
@@ -554,8 +555,8 @@ cudaError_t launch_paged_evict(const PagedEvictLaunch& a, cudaStream_t stream) {
   p.n_sink = a.n_sink;
   p.cap = move_cap(a.max_len, a.budget);
   p.in_place = a.mass_out == c.mass;
-  // Few rows can move: the selecting CTA moves them itself (32 x 8 units, 2112 slots to 2048: 14.7 us
-  // against 18.3).
+  // Few rows can move: the selecting CTA moves them itself (32 x 8 units, 2112 slots to 2048: 11.0 us
+  // against 13.0).
   p.fused = p.cap <= kMostFused;
   p.lengths_apart = p.fused && a.seq_len_out != a.seq_len;
   const size_t lists = round256((size_t)units * p.cap * 4);
