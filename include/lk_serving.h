@@ -94,8 +94,9 @@ lk_status lk_paged_append(const lk_paged_cache* cache, const int32_t* page_table
  * workspace: lk_paged_decode_workspace_bytes(...) bytes, 256-byte aligned,
  *   any contents; calls that may run at the same time need their own.
  * Scores, softmax statistics and the output sum are fp32; the weights p meet
- *   V as a sum of two 16-bit terms (relative rounding at most 2^-16; for fp16
- *   and int8 caches not below 2^-35 of their sum).
+ *   V as a sum of two 16-bit terms (relative rounding at most 2^-16, fp16 and
+ *   int8 caches 2^-22 but not below 2^-35 of their sum), for an LK_F32 out of a
+ *   bf16 cache of three (2^-24).
  *   Weights are held at up to 2^4 (fp16 and int8 caches: 2^14), and that times
  *   seq_len |v| has to stay in fp32's range; an infinity in an attended V row
  *   makes its dim NaN.

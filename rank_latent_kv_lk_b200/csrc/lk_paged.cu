@@ -34,7 +34,10 @@
 // codes of a token (Q is laid out in that order of dims), ldmatrix.trans two
 // dims of two tokens, whose even and odd bytes are the rows of one product.
 // The weights are split into two 16-bit terms (high and remainder), so their
-// rounding is 2^-16 (bf16) or 2^-22 (fp16) relative.  fp16 weights are held
+// rounding is 2^-16 (bf16) or 2^-22 (fp16) relative.  An fp32 output of a bf16
+// cache gets a third term (2^-24); a 16-bit one would round it away: its error
+// against 64 bits is the same without (relative 1.68e-3 in 2-norm, 9.5e-7 of
+// it from the two terms).  fp16 weights are held
 // 2^10 times larger, which keeps small ones out of the subnormals: the largest
 // weight is 2^14, the sum at least 2^10 and the smallest step 2^-24.
 // int8 caches: codes are exact in fp16 (byte permute into the mantissa of
@@ -76,6 +79,7 @@ struct PagedParams {
   int resident;     // CTAs the GPU holds
   // one CTA a unit (grid = units): the output and mass are written here
   int direct, unit_blocks, out_dtype;
+  int third;        // bf16 weights in three terms
   int ring;         // bytes of a warp's ring
   void* out;
   float* mass;
@@ -144,6 +148,12 @@ __host__ __device__ inline int64_t working_ctas(int64_t N, int64_t resident) {
 LK_DEVICE int64_t quotient(int64_t a, int64_t c) {
   if (((a | c) >> 32) == 0) return (uint32_t)a / (uint32_t)c;
   return a / c;
+}
+
+// What the two bf16 terms of a weight leave.
+LK_DEVICE float third_term(float a) {
+  const float r = a - lk_bf16_to_f32(lk_f32_to_bf16(a));
+  return r - lk_bf16_to_f32(lk_f32_to_bf16(r));
 }
 
 // Four outputs in the call's type.
@@ -618,9 +628,17 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
           }
         }
       }
-      uint32_t ph[NT][2], pl[NT][2];
+      uint32_t ph[NT][2], pl[NT][2], px[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (DT == DT_BF16) {
+          if (p.third) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              px[nt][i] =
+                  movmatrix_trans(lk_pack_bf16x2(third_term(c[nt][2 * i]), third_term(c[nt][2 * i + 1])));
+          }
+        }
         if constexpr (DT == DT_I8) {
           c[nt][0] *= vs0;
           c[nt][1] *= vs0;
@@ -662,6 +680,18 @@ __global__ void __launch_bounds__(W * 32, Shape<VC, NT, DT, W>::kMinCtas)
             float (&acc)[4] = o[v][nt];
             mma16816<DT>(acc, v4[0], v4[2], v4[1], v4[3], ph[nt][0], ph[nt][1]);
             mma16816<DT>(acc, v4[0], v4[2], v4[1], v4[3], pl[nt][0], pl[nt][1]);
+          }
+        }
+      }
+      if constexpr (DT == DT_BF16) {
+        if (p.third) {  // in a loop of its own: the one above keeps its registers and instructions
+#pragma unroll
+          for (int v = 0; v < S::kCh / 2; ++v) {
+            if (v >= steps) break;
+            uint32_t v4[4];
+            ldmatrix4<true>(v4, st + kTok * S::kRowB + f_at + (f_ch ^ (v << 5)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<DT>(o[v][nt], v4[0], v4[2], v4[1], v4[3], px[nt][0], px[nt][1]);
           }
         }
       }
@@ -1241,6 +1271,7 @@ cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream)
   p.unit_blocks = r.unit_blocks;
   p.out = a.out;
   p.out_dtype = a.out_dtype;
+  p.third = dt == DT_BF16 && a.out_dtype == LK_F32;
   p.mass = a.accumulate ? c.mass : nullptr;
   p.offset = dt == DT_BF16 ? 0.0f : kHeld;
   cudaError_t e;

@@ -280,3 +280,28 @@ def test_append_then_attend_is_the_longer_cache():
     want, tol, mass, mtol = attention(pages, q, 128 ** -0.5, want_mass=True)
     check(got, want, tol + 1e-30, "out")
     check(cache.mass.cpu()[pages.live], mass[pages.live], mtol[pages.live] + 1e-30, "mass")
+
+
+@pytest.mark.parametrize("lens", [[2] * 64, [600, 513]], ids=["one CTA a unit", "split"])
+def test_fp32_outputs_of_a_bf16_cache_keep_fp32_weights(lens):
+    # Scores that are exact products: token 0 scores 0 and holds zeros, token 1 scores -q, the rest nothing.  Then
+    # out = w v / (1 + w), w = exp(-q), q <= 1/4, and what is off relative to it, in units of 2^-22: the scaled score
+    # (log2 e and one product, 0.36 2^-23 in log2) 0.13, the exponential 1, the weight's three terms 0.25 and their
+    # sum 1.5, the sum of weights over warps and pieces 2, the quotient 0.5: below 6.  (Weights in two bf16 terms are
+    # off by up to 2^-17.6, 21 of these.)
+    pages = Pages(lens, 2, 16, 16, BF, seed=21)
+    q = torch.zeros(len(lens), 8, 16)
+    q[:, :, 0] = 0.05 + 0.2 * torch.rand(len(lens), 8, generator=pages.g)
+    q = q.to(BF)
+    pages.k[pages.live] = 0
+    for b, n in enumerate(lens):
+        for t in range(1, n):
+            pages.k[pages.table[b, t // 16], :, t % 16, 0] = -1.0 if t == 1 else -1e38
+        pages.v[pages.table[b, 0], :, 0] = 0
+    got, _ = run(pages, q, scale=1.0)
+    want = torch.zeros(len(lens), 8, 16, dtype=torch.float64)
+    for b in range(len(lens)):
+        for h in range(8):
+            w = math.exp(-float(q[b, h, 0]))
+            want[b, h] = w / (1 + w) * pages.dense(b, h // 4)[1][1]
+    check(got, want, 6 * 2.0 ** -22 * want.abs() + 1e-30, "fp32 out")
