@@ -84,6 +84,12 @@ struct PagedCache {
   PagedCache(Tensor k_, Tensor v_, OptTensor ks, OptTensor vs, OptTensor m, OptTensor p)
       : k(std::move(k_)), v(std::move(v_)), k_scale(std::move(ks)), v_scale(std::move(vs)), mass(std::move(m)),
         pos(std::move(p)), dev(k.device()) {
+    describe();
+  }
+
+  // The descriptor, from the tensors as they are: a call that kept the pointers and sizes of an earlier one would
+  // miss a tensor whose storage or shape was changed in place.
+  void describe() {
     const auto t = k.scalar_type();
     TORCH_CHECK_VALUE(k.dim() == 4 && k.is_cuda(),
                       "k: a CUDA tensor [n_pages, n_kv_heads, page_size, head_dim] is needed");
@@ -142,9 +148,10 @@ int32_t as_i32(const char* name, int64_t v) {
   return (int32_t)v;
 }
 
-void paged_append(const PagedCache& c, const Tensor& table, const Tensor& k_new, const Tensor& v_new,
+void paged_append(PagedCache& c, const Tensor& table, const Tensor& k_new, const Tensor& v_new,
                   const Tensor& seq_len, const OptTensor& next_pos, const OptTensor& new_len,
                   const OptTensor& seq_len_out, const OptTensor& next_pos_out) {
+  c.describe();
   const c10::cuda::CUDAGuard guard(c.dev);
   const int64_t step = c.token_step("k_new", k_new);
   TORCH_CHECK_VALUE(v_new.sizes() == k_new.sizes() && v_new.scalar_type() == k_new.scalar_type() &&
@@ -164,9 +171,10 @@ void paged_append(const PagedCache& c, const Tensor& table, const Tensor& k_new,
                         next_pos_out ? ptr<int32_t>(next_pos_out) : ptr<int32_t>(next_pos), stream_of(c.dev)));
 }
 
-Tensor paged_decode_attn(const PagedCache& c, const Tensor& table, const Tensor& q, const Tensor& seq_len,
+Tensor paged_decode_attn(PagedCache& c, const Tensor& table, const Tensor& q, const Tensor& seq_len,
                          int64_t max_seq_len, std::optional<double> softmax_scale, bool accumulate,
                          const OptTensor& out, std::optional<at::ScalarType> out_dtype) {
+  c.describe();
   const c10::cuda::CUDAGuard guard(c.dev);
   TORCH_CHECK_VALUE(q.dim() == 3 && q.size(2) == c.d.head_dim && q.device() == c.dev, "q: [batch, n_heads, ",
                     c.d.head_dim, "] on ", c.dev, " is needed, not ", q.sizes(), " on ", q.device());
@@ -188,9 +196,10 @@ Tensor paged_decode_attn(const PagedCache& c, const Tensor& table, const Tensor&
   return o;
 }
 
-void paged_evict(const PagedCache& c, const Tensor& table, const Tensor& seq_len, const Tensor& next_pos,
+void paged_evict(PagedCache& c, const Tensor& table, const Tensor& seq_len, const Tensor& next_pos,
                  int64_t max_seq_len, int64_t budget, int64_t window, int64_t n_sink, const OptTensor& mass_out,
                  const OptTensor& pos_out, const OptTensor& seq_len_out) {
+  c.describe();
   const c10::cuda::CUDAGuard guard(c.dev);
   TORCH_CHECK_VALUE(c.mass.has_value(), "eviction needs a cache with mass and pos");
   TORCH_CHECK_VALUE(seq_len.dim() == 1, "seq_len: [batch] is needed");
@@ -247,6 +256,8 @@ Tensor w4_linear(const W4& w, const Tensor& x, const OptTensor& residual, const 
   TORCH_CHECK_VALUE(x.dim() == 2 && x.size(1) == w.k_in && x.stride(1) == 1 && x.device() == w.dev, "x: [m, ", w.k_in,
                     "] with contiguous rows on ", w.dev, " is needed, not ", x.sizes(), " with strides ", x.strides(),
                     " on ", x.device());
+  TORCH_CHECK_VALUE((size_t)w.packed.nbytes() == lk_w4_packed_bytes(w.n_out, w.k_in, w.group, w.gated),
+                    "the packed weight was resized");
   const int64_t m = x.size(0);
   const int64_t shape[2] = {m, w.n_out};
   same("residual", residual, shape, x.scalar_type(), w.dev);
@@ -292,7 +303,13 @@ std::pair<Tensor, OptTensor> rmsnorm_gate_residual(const Tensor& y, const Tensor
 
 PYBIND11_MODULE(_serving_ext, m) {
   py::class_<PagedCache>(m, "PagedCache")
-      .def(py::init<Tensor, Tensor, OptTensor, OptTensor, OptTensor, OptTensor>());
+      .def(py::init<Tensor, Tensor, OptTensor, OptTensor, OptTensor, OptTensor>())
+      .def_readonly("k", &PagedCache::k)
+      .def_readonly("v", &PagedCache::v)
+      .def_readonly("k_scale", &PagedCache::k_scale)
+      .def_readonly("v_scale", &PagedCache::v_scale)
+      .def_readonly("mass", &PagedCache::mass)
+      .def_readonly("pos", &PagedCache::pos);
   py::class_<W4>(m, "W4")
       .def(py::init<const Tensor&, const Tensor&, const OptTensor&, const OptTensor&>())
       .def_readonly("packed", &W4::packed)

@@ -25,6 +25,24 @@ def _on(stream, device, fn, *args):
         return fn(*args)
 
 
+_TENSORS = ("k", "v", "k_scale", "v_scale", "mass", "pos")
+
+
+def _tensor(name):
+    """A tensor of a PagedKVCache: assigning one replaces it for every later call."""
+    def get(self):
+        return getattr(self._c, name)
+
+    def put(self, t):
+        self._set(*[t if n == name else getattr(self._c, n) for n in _TENSORS])
+
+    return property(get, put)
+
+
+def _size(i):
+    return property(lambda self: self._c.k.shape[i])
+
+
 class PagedKVCache:
     """Paged K and V of one layer: pages of `page_size` rows per kv head.
 
@@ -53,11 +71,14 @@ class PagedKVCache:
         self._set(k, v, k_scale, v_scale, mass, pos)
         return self
 
-    def _set(self, k, v, k_scale, v_scale, mass, pos):
-        self._c = _ext.PagedCache(k, v, k_scale, v_scale, mass, pos)
-        self.k, self.v, self.k_scale, self.v_scale, self.mass, self.pos = k, v, k_scale, v_scale, mass, pos
-        self.device, self.dtype = k.device, k.dtype
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+    def _set(self, *tensors):
+        self._c = _ext.PagedCache(*tensors)  # refuses tensors that do not fit together
+
+    # The binding's own tensors, so that what is shown here is what the calls use.
+    k, v, k_scale, v_scale, mass, pos = (_tensor(n) for n in _TENSORS)
+    device = property(lambda self: self._c.k.device)
+    dtype = property(lambda self: self._c.k.dtype)
+    n_pages, n_kv_heads, page_size, head_dim = (_size(i) for i in range(4))
 
 
 def paged_append(cache, page_table, k_new, v_new, seq_len, next_pos=None, new_len=None, seq_len_out=None,
@@ -110,6 +131,10 @@ def paged_evict(cache, page_table, seq_len, next_pos, max_seq_len, budget, windo
                      seq_len_out)
 
 
+def _shown(name):
+    return property(lambda self: getattr(self._c, name))
+
+
 class W4Weight:
     """4-bit weight [n_out, k_in] laid out for w4_linear: codes uint8 [n_out,
     k_in / 2] (two's-complement nibbles, low nibble = even input), scales fp16
@@ -117,8 +142,9 @@ class W4Weight:
     the same sizes the product is silu(x gate^T) * (x up^T)."""
 
     def __init__(self, codes, scales, up_codes=None, up_scales=None):
-        self._c = c = _ext.W4(codes, scales, up_codes, up_scales)
-        self.packed, self.n_out, self.k_in, self.group, self.gated = c.packed, c.n_out, c.k_in, c.group, c.gated
+        self._c = _ext.W4(codes, scales, up_codes, up_scales)
+
+    packed, n_out, k_in, group, gated = (_shown(n) for n in ("packed", "n_out", "k_in", "group", "gated"))
 
 
 def w4_linear(w, x, residual=None, y=None, y_dtype=None, stream=None):

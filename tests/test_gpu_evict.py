@@ -193,3 +193,73 @@ def test_lengths_between_the_calls_of_a_batch():
     assert seq.tolist() == [64, 0, 10]
     for n in ("k", "v", "mass", "pos"):
         torch.testing.assert_close(getattr(cache, n).cpu(), getattr(pages, n), rtol=0, atol=0, equal_nan=True)
+
+
+def test_outputs_apart_take_the_caches_place():
+    # an eviction into arrays of their own, which then become the cache's: what follows is what follows one in place
+    import rank_latent_kv_lk_b200 as lk
+    caches = []
+    for apart in (False, True):
+        pages = Pages([260, 100, 300], 2, 64, 16, BF, seed=6, mass=True, extra=1)
+        cache, seq, table = pages.cuda(), pages.seq(), pages.table.cuda()
+        nxt = seq.clone()
+        g = torch.Generator().manual_seed(1)
+        q = torch.randn(3, 4, 64, generator=g).to(BF).cuda()
+        k, v = torch.randn(2, 3, 1, 2, 64, generator=g).to(BF).cuda()
+        if apart:
+            m, p = cache.mass.clone(), cache.pos.clone()
+            lk.paged_evict(cache, table, seq, nxt, 301, 90, window=5, mass_out=m, pos_out=p)
+            cache.mass, cache.pos = m, p
+            assert cache.mass is m and cache.pos is p
+        else:
+            lk.paged_evict(cache, table, seq, nxt, 301, 90, window=5)
+        lk.paged_append(cache, table, k, v, seq, nxt)
+        out = lk.paged_decode_attn(cache, table, q, seq, 301, accumulate=True)
+        lk.paged_evict(cache, table, seq, nxt, 301, 50, window=5)
+        caches.append((pages, cache, out, seq.tolist()))
+    (pages, a, out_a, n_a), (_, b, out_b, n_b) = caches
+    assert torch.equal(out_a, out_b) and n_a == n_b == [50] * 3
+    for name in ("k", "v", "mass", "pos"):
+        x, y = getattr(a, name).cpu(), getattr(b, name).cpu()
+        for s in range(3):
+            for h in range(2):
+                assert torch.equal(pages.rows(x, s, h, 50), pages.rows(y, s, h, 50)), name
+
+
+def test_tensors_of_a_cache_and_a_weight():
+    import rank_latent_kv_lk_b200 as lk
+    cache = lk.PagedKVCache(8, 16, 2, 64, mass=True)
+    assert (cache.n_pages, cache.n_kv_heads, cache.page_size, cache.head_dim) == (8, 2, 16, 64)
+    before = cache.k, cache.mass
+    with pytest.raises(ValueError):
+        cache.mass = None                                  # positions without weights
+    with pytest.raises(ValueError):
+        cache.k = torch.zeros(9, 2, 16, 64, dtype=BF, device="cuda")
+    with pytest.raises(TypeError):
+        cache.mass = cache.mass.half()
+    with pytest.raises(ValueError):
+        cache.v = cache.v.cpu()
+    with pytest.raises(AttributeError):
+        cache.page_size = 32
+    assert cache.k is before[0] and cache.mass is before[1]
+    # storage changed in place: the calls see it, and refuse sizes that no longer fit
+    table = torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    seq, nxt = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    one = torch.ones(1, 1, 2, 64, dtype=BF, device="cuda")
+    cache.v.set_(torch.full_like(cache.v, 3))
+    lk.paged_append(cache, table, one, one, seq, nxt)
+    out = lk.paged_decode_attn(cache, table, one[:, 0], seq, 32)
+    assert (out == 1).all() and (cache.v[0, :, 0] == 1).all() and (cache.v[0, :, 1] == 3).all()
+    cache.pos.resize_(8, 2, 8)
+    for call in (lambda: lk.paged_append(cache, table, one, one, seq, nxt),
+                 lambda: lk.paged_decode_attn(cache, table, one[:, 0], seq, 32),
+                 lambda: lk.paged_evict(cache, table, seq, nxt, 32, 8)):
+        with pytest.raises(ValueError):
+            call()
+    w = lk.W4Weight(torch.zeros(16, 32, dtype=torch.uint8, device="cuda"),
+                    torch.zeros(16, 1, dtype=torch.float16, device="cuda"))
+    with pytest.raises(AttributeError):
+        w.packed = torch.zeros(1)
+    w.packed.resize_(16)
+    with pytest.raises(ValueError):
+        lk.w4_linear(w, torch.zeros(1, 64, dtype=BF, device="cuda"))
