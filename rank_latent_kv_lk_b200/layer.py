@@ -25,8 +25,6 @@ import torch
 
 from .api import (LatentCache, LowrankWeight, latent_decode_step, lowrank_linear, quantize_rows_i8,
                   rmsnorm_quant_i8, swiglu_quant_i8)
-from .serving import (PagedKVCache, W4Weight, paged_append, paged_decode_attn, paged_evict, rmsnorm_gate_residual,
-                      w4_linear)
 
 
 def dense_weight(W, s, device):
@@ -107,31 +105,35 @@ class W4PagedDecoderLayer:
 
     def __init__(self, weights, n_heads, n_kv_heads, head_dim, n_pages, page_size, cache_dtype=torch.bfloat16,
                  mass=False, eps=1e-5, device="cuda"):
+        # here and not above: W8A8DecoderLayer does without the serving operators' binding
+        from . import serving
+        self._op = serving
         self.n_heads, self.n_kv_heads, self.head_dim, self.eps = n_heads, n_kv_heads, head_dim, eps
 
         def w4(*names):
-            return W4Weight(*[t.to(device) for n in names for t in weights[n]])
+            return serving.W4Weight(*[t.to(device) for n in names for t in weights[n]])
 
         self.qkv, self.o, self.gate_up, self.down = w4("qkv"), w4("o"), w4("gate", "up"), w4("down")
         self.norm = {k: None if weights.get(k) is None else weights[k].to(device)
                      for k in ("norm_ffn", "norm_next", "post_attn", "post_ffn", "gate_attn", "gate_ffn")}
-        self.cache = PagedKVCache(n_pages, page_size, n_kv_heads, head_dim, cache_dtype, mass, device)
+        self.cache = serving.PagedKVCache(n_pages, page_size, n_kv_heads, head_dim, cache_dtype, mass, device)
 
     def step(self, x, h, page_table, seq_len, max_seq_len, next_pos=None):
         """x, h: [B, E]; page_table, seq_len, next_pos: device int32 (lengths and positions advance by one in
         place); max_seq_len: host bound on the lengths after the step."""
-        B, nh, nk, D, n = x.shape[0], self.n_heads, self.n_kv_heads, self.head_dim, self.norm
-        qkv = w4_linear(self.qkv, h)
+        B, nh, nk, D, n, op = x.shape[0], self.n_heads, self.n_kv_heads, self.head_dim, self.norm, self._op
+        qkv = op.w4_linear(self.qkv, h)
         q = qkv[:, :nh * D].view(B, nh, D)
         k = qkv[:, nh * D:(nh + nk) * D].view(B, 1, nk, D)
         v = qkv[:, (nh + nk) * D:].view(B, 1, nk, D)
-        paged_append(self.cache, page_table, k, v, seq_len, next_pos)
-        a = paged_decode_attn(self.cache, page_table, q, seq_len, max_seq_len, accumulate=self.cache.mass is not None)
-        y = w4_linear(self.o, a.view(B, nh * D))
-        x, h = rmsnorm_gate_residual(y, x, n["post_attn"], n["gate_attn"], 1.0, n["norm_ffn"], self.eps)
-        y = w4_linear(self.down, w4_linear(self.gate_up, h))
-        return rmsnorm_gate_residual(y, x, n["post_ffn"], n["gate_ffn"], 1.0, n["norm_next"], self.eps)
+        op.paged_append(self.cache, page_table, k, v, seq_len, next_pos)
+        a = op.paged_decode_attn(self.cache, page_table, q, seq_len, max_seq_len,
+                                 accumulate=self.cache.mass is not None)
+        y = op.w4_linear(self.o, a.view(B, nh * D))
+        x, h = op.rmsnorm_gate_residual(y, x, n["post_attn"], n["gate_attn"], 1.0, n["norm_ffn"], self.eps)
+        y = op.w4_linear(self.down, op.w4_linear(self.gate_up, h))
+        return op.rmsnorm_gate_residual(y, x, n["post_ffn"], n["gate_ffn"], 1.0, n["norm_next"], self.eps)
 
     def evict(self, page_table, seq_len, next_pos, max_seq_len, budget, window=0, n_sink=0):
         """Cut the sequences to `budget` cached tokens per kv head (lengths in place)."""
-        paged_evict(self.cache, page_table, seq_len, next_pos, max_seq_len, budget, window, n_sink)
+        self._op.paged_evict(self.cache, page_table, seq_len, next_pos, max_seq_len, budget, window, n_sink)

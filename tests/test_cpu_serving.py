@@ -4,6 +4,8 @@ touched (a call that got through would report LK_ERR_CUDA here)."""
 import ctypes as C
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -244,3 +246,14 @@ def test_wrappers_refuse_tensors_of_the_host(L):
         lk.rmsnorm_gate_residual(k[0, 0], k[0, 0])
     with pytest.raises(ValueError):
         lk.W4Weight(torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.float16))
+
+
+def test_the_latent_layer_does_without_the_serving_binding(L):
+    # as where the binding does not fit the installed torch: W8A8DecoderLayer needs only liblk.so
+    code = ("import sys; sys.modules['rank_latent_kv_lk_b200._serving_ext'] = None\n"
+            "from rank_latent_kv_lk_b200.layer import W8A8DecoderLayer, W4PagedDecoderLayer\n"
+            "try:\n    W4PagedDecoderLayer({}, 8, 2, 64, 8, 16)\n"
+            "except ImportError:\n    print('refused')\n")
+    p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr
+    assert p.stdout.split() == ["refused"]
