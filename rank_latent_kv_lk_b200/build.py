@@ -7,7 +7,8 @@ Each .cu file compiles to an object under ``_build/`` (in parallel), then the
 objects link into ``rank_latent_kv_lk_b200/liblk.so``; the torch binding of the
 serving operators (``csrc/lk_serving_py.cpp``) compiles with g++ into
 ``_serving_ext.so`` beside it.  Objects are rebuilt when their source or any
-header is newer.  IEEE fp32 semantics are kept
+header is newer, the binding also for another Python or torch than it was built
+for (kept in ``_build/``); without torch it is left out.  IEEE fp32 semantics are kept
 (no fast-math, no flush-to-zero): the latent quantiser is bit-exact.
 """
 from __future__ import annotations
@@ -62,11 +63,26 @@ def _compile(src, obj, verbose, extra):
 
 def _build_ext(force, verbose):
     """The torch binding; links against liblk.so beside it."""
-    deps = [EXT_SRC, os.path.join(INCLUDE, "lk.h"), os.path.join(INCLUDE, "lk_serving.h")]
-    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(d) for d in deps):
-        return
+    import importlib.metadata
+    import importlib.util
     import sysconfig
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        print("torch is not installed: liblk.so stands alone, without the binding of the serving operators", flush=True)
+        return
+    deps = [EXT_SRC, os.path.join(INCLUDE, "lk.h"), os.path.join(INCLUDE, "lk_serving.h")]
+    built_for = f"python {sys.version_info[:2]} torch {importlib.metadata.version('torch')} {spec.origin}\n"
+    stamp = os.path.join(BUILD, "serving_ext.txt")
 
+    def stamped():
+        if not os.path.exists(stamp):
+            return ""
+        with open(stamp) as f:
+            return f.read()
+
+    if not force and os.path.exists(EXT) and stamped() == built_for and \
+            os.path.getmtime(EXT) >= max(os.path.getmtime(d) for d in deps):
+        return
     import torch
     from torch.utils import cpp_extension
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
@@ -83,6 +99,8 @@ def _build_ext(force, verbose):
     if p.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(EXT_SRC)}:\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, EXT)
+    with open(stamp, "w") as f:
+        f.write(built_for)
 
 
 def build(force=False, verbose=False, extra_flags=()):

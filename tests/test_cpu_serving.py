@@ -4,6 +4,7 @@ touched (a call that got through would report LK_ERR_CUDA here)."""
 import ctypes as C
 import os
 import re
+import shutil
 import subprocess
 import sys
 
@@ -257,3 +258,33 @@ def test_the_latent_layer_does_without_the_serving_binding(L):
     p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert p.returncode == 0, p.stderr
     assert p.stdout.split() == ["refused"]
+
+
+def test_the_binding_is_built_again_for_another_torch(L, tmp_path, monkeypatch):
+    import importlib.metadata
+    import importlib.util
+
+    import __graft_entry__
+    b = __graft_entry__._load_builder()
+    shutil.copy2(b.EXT, tmp_path / "ext.so")
+    monkeypatch.setattr(b, "EXT", str(tmp_path / "ext.so"))
+    monkeypatch.setattr(b, "BUILD", str(tmp_path))
+    built = []
+
+    def compiler(cmd, **kw):
+        built.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(b.subprocess, "run", compiler)
+    b._build_ext(True, False)
+    b._build_ext(False, False)
+    assert len(built) == 1                                    # nothing changed
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.1")
+    b._build_ext(False, False)
+    b._build_ext(False, False)
+    assert len(built) == 2
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda n, *a: None if n == "torch" else find(n, *a))
+    b._build_ext(True, False)                                 # no torch: the library alone
+    assert len(built) == 2
