@@ -8,6 +8,10 @@ refuses raises LkError.  Every call runs on its tensors' device and on that
 device's current stream, or on `stream`.  Outputs and scratch memory come from
 torch's allocator per call, so calls on several streams and captured graphs
 share none.
+
+A call on `stream` is ordered with nothing else: the caller makes that stream
+wait for the inputs (stream.wait_stream) and waits for it before using the
+result.  Both may be freed without waiting.
 """
 from __future__ import annotations
 
@@ -18,11 +22,30 @@ from . import _serving_ext as _ext
 
 
 def _on(stream, device, fn, *args):
-    """The call with `stream` current, which has to be the tensors' device's."""
+    """The call with `stream` current, which has to be the tensors' device's.  The memory of the inputs, which another
+    stream's pool may own, is not given out again before the call is done, nor the result's before the caller's stream
+    is done with it."""
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    caller = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
-        return fn(*args)
+        out = fn(*args)
+    if stream != caller:
+        for a in args:
+            for t in _tensors_of(a):
+                t.record_stream(stream)
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(caller)
+    return out
+
+
+def _tensors_of(a):
+    if isinstance(a, torch.Tensor):
+        return (a,)
+    if isinstance(a, PagedKVCache):
+        return tuple(t for t in (getattr(a, n) for n in _TENSORS) if t is not None)
+    return (a.packed,) if isinstance(a, W4Weight) else ()
 
 
 _TENSORS = ("k", "v", "k_scale", "v_scale", "mass", "pos")

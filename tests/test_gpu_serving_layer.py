@@ -275,3 +275,50 @@ def test_wrappers_refuse_wrong_tensors():
             lk.rmsnorm_gate_residual(**dict(dict(y=y, x=y), **bad))
     with pytest.raises(ValueError):
         lk.rmsnorm_gate_residual(y.t(), y.t())
+
+
+@pytest.mark.parametrize("op", ["attention", "product", "norm"])
+def test_memory_of_a_call_on_another_stream(op):
+    # The input is freed, and its memory asked for again, while the call still waits on its stream; then the result,
+    # while the caller's stream still waits to read it.
+    import rank_latent_kv_lk_b200 as lk
+    g = torch.Generator().manual_seed(2)
+    if op == "attention":
+        cache = lk.PagedKVCache.from_tensors(*torch.randn(2, 8, 4, 16, 64, generator=g).to(BF).cuda())
+        table = torch.arange(8, dtype=torch.int32, device="cuda").expand(64, 8).contiguous()
+        seq = torch.full((64,), 128, dtype=torch.int32, device="cuda")
+        x = torch.randn(64, 32, 64, generator=g).to(BF).cuda()
+
+        def call(x, stream=None):
+            return lk.paged_decode_attn(cache, table, x, seq, 128, stream=stream)
+    elif op == "product":
+        w = lk.W4Weight(*(t.cuda() for t in w4(4096, 4096, g)))
+        x = torch.randn(32, 4096, generator=g).to(BF).cuda()
+
+        def call(x, stream=None):
+            return lk.w4_linear(w, x, stream=stream)
+    else:
+        x = torch.randn(32, 4096, generator=g).to(BF).cuda()
+        one = torch.ones(4096, dtype=BF, device="cuda")
+
+        def call(x, stream=None):
+            return lk.rmsnorm_gate_residual(x, x, w_pre=one, stream=stream)[1]
+    neg = -2 * x
+    want, other = call(x), call(neg)
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    mine = x.clone()
+    side.wait_stream(here)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = call(mine, stream=side)
+    del mine
+    new = [torch.full_like(x, 7) for _ in range(4)]
+    here.wait_stream(side)
+    torch.cuda._sleep(20_000_000)
+    seen = got.clone()
+    del got
+    more = [call(neg, stream=side) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(seen, want)
+    assert all(torch.equal(m, other) for m in more)
+    assert all((n == 7).all() for n in new)
