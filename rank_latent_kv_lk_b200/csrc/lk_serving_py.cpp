@@ -164,6 +164,7 @@ void paged_append(PagedCache& c, const Tensor& table, const Tensor& k_new, const
   c.counts("new_len", new_len, batch);
   c.counts("seq_len_out", seq_len_out, batch);
   c.counts("next_pos_out", next_pos_out, batch);
+  if (batch == 0) return;
   check(lk_paged_append(&c.d, ptr<int32_t>(table), as_i32("batch", batch), width, ptr(k_new), ptr(v_new),
                         dtype_of("k_new", k_new.scalar_type(), true), as_i32("token spacing", step),
                         as_i32("n_new", k_new.size(1)), ptr<int32_t>(new_len), ptr<int32_t>(seq_len),
@@ -187,6 +188,7 @@ Tensor paged_decode_attn(PagedCache& c, const Tensor& table, const Tensor& q, co
   Tensor o = out ? *out : empty(q.sizes(), out_dtype.value_or(q.scalar_type()), c.dev);
   const lk_dtype qt = dtype_of("q", q.scalar_type(), true), ot = dtype_of("out", o.scalar_type(), false);
   const int32_t b = as_i32("batch", batch), h = as_i32("n_heads", heads), m = as_i32("max_seq_len", max_seq_len);
+  if (b == 0) return o;
   const size_t need = lk_paged_decode_workspace_bytes(&c.d, b, h, m, accumulate);
   const Tensor ws = scratch(need, c.dev);
   check(lk_paged_decode_attn(&c.d, ptr<int32_t>(table), b, width, ptr(q), qt, h,
@@ -212,6 +214,7 @@ void paged_evict(PagedCache& c, const Tensor& table, const Tensor& seq_len, cons
   same("mass_out", mass_out, rows, at::kFloat, c.dev);
   same("pos_out", pos_out, rows, at::kInt, c.dev);
   const int32_t b = as_i32("batch", batch), m = as_i32("max_seq_len", max_seq_len), n = as_i32("budget", budget);
+  if (b == 0) return;
   const size_t need = lk_paged_evict_workspace_bytes(&c.d, b, m, n);
   const Tensor ws = scratch(need, c.dev);
   check(lk_paged_evict(&c.d, ptr<int32_t>(table), b, width, ptr<int32_t>(seq_len), ptr<int32_t>(next_pos), m, n,

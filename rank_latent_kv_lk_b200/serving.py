@@ -7,7 +7,7 @@ the calls stand in the binding (csrc/lk_serving_py.cpp); what the library
 refuses raises LkError.  Every call runs on its tensors' device and on that
 device's current stream, or on `stream`.  Outputs and scratch memory come from
 torch's allocator per call, so calls on several streams and captured graphs
-share none.
+share none.  No sequences or rows at all are no error: nothing is done.
 
 A call on `stream` is ordered with nothing else: the caller makes that stream
 wait for the inputs (stream.wait_stream) and waits for it before using the

@@ -322,3 +322,22 @@ def test_memory_of_a_call_on_another_stream(op):
     assert torch.equal(seen, want)
     assert all(torch.equal(m, other) for m in more)
     assert all((n == 7).all() for n in new)
+
+
+def test_no_sequences():
+    # as products and norms of no rows: an empty result, and nothing done
+    import rank_latent_kv_lk_b200 as lk
+    layer, _, _, _, _, _ = setup(1, True)
+    before = [t.clone() for t in (layer.cache.k, layer.cache.mass)]
+    table = torch.empty(0, 6, dtype=torch.int32, device="cuda")
+    n = torch.empty(0, dtype=torch.int32, device="cuda")
+    x = torch.empty(0, E, dtype=BF, device="cuda")
+    launches = lk.kernel_launches()
+    out = layer.step(x, x, table, n, 64, n.clone())
+    layer.evict(table, n, n.clone(), 64, 8)
+    assert out[0].shape == out[1].shape == (0, E) and lk.kernel_launches() == launches
+    q = torch.empty(0, NH, D, dtype=BF, device="cuda")
+    assert lk.paged_decode_attn(layer.cache, table, q, n, 64, out_dtype=torch.float32).shape == (0, NH, D)
+    with pytest.raises(ValueError):
+        lk.paged_decode_attn(layer.cache, table, q[:, :, :16], n, 64)
+    assert torch.equal(before[0], layer.cache.k) and torch.equal(before[1], layer.cache.mass)
