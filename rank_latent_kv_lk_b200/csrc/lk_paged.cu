@@ -1162,7 +1162,7 @@ Plan make_plan(int batch, int n_kv, int n_heads, int D, int dtype, int max_len, 
   r.resident = num_sms * ctas_per_sm(r.vc, r.nt, dt);
   r.grid = (int)working_ctas(r.blocks, r.resident);
   r.unit_blocks = (max_len + kTok - 1) / kTok;
-  r.direct = max_len <= std::max(kDirect, std::min(kDirectMost, kDirectPer * r.units)) && (!accumulate || r.nch == 1);
+  r.direct = max_len <= std::max(kDirect, (int)std::min<int64_t>(kDirectMost, (int64_t)kDirectPer * r.units)) && (!accumulate || r.nch == 1);
   // Eight warps a CTA where every CTA has an SM to itself (128 units of 1024 tokens: 15.2 us against 20.0; 256
   // units: 28.5 against 25.4), if there are blocks for them.
   r.wide = r.direct && r.units <= num_sms && r.unit_blocks > kWarps &&

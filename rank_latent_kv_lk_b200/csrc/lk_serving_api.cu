@@ -49,6 +49,8 @@ extern "C" {
 
 // ---------------------------------------------------------------- paged key-value cache
 namespace {
+constexpr int64_t kMaxSlots = (int64_t)1 << 30;  // of a sequence: sizes made from it stay within 32 bits
+
 bool is_16bit(lk_dtype t) { return t == LK_BF16 || t == LK_F16; }
 
 lk_status check_paged(const lk_paged_cache* c, int32_t batch, int32_t table_width) {
@@ -65,7 +67,7 @@ lk_status check_paged(const lk_paged_cache* c, int32_t batch, int32_t table_widt
   if ((int64_t)c->n_pages * c->n_kv_heads * c->page_size >= (int64_t)1 << 31)
     return fail(LK_ERR_SHAPE, "n_pages * n_kv_heads * page_size must stay below 2^31");
   if (batch < 1 || table_width < 1) return fail(LK_ERR_SHAPE, "batch %d or table_width %d < 1", batch, table_width);
-  if ((int64_t)table_width * c->page_size > (int64_t)1 << 30)
+  if ((int64_t)table_width * c->page_size > kMaxSlots)
     return fail(LK_ERR_SHAPE, "table_width * page_size must be at most 2^30");
   if ((int64_t)batch * LK_MAX_HEADS >= (int64_t)1 << 31) return fail(LK_ERR_SHAPE, "batch %d too large", batch);
   return LK_OK;
@@ -149,7 +151,7 @@ lk_status lk_paged_append(const lk_paged_cache* cache, const int32_t* page_table
 
 size_t lk_paged_decode_workspace_bytes(const lk_paged_cache* cache, int32_t batch, int32_t n_heads,
                                        int32_t max_seq_len, int32_t accumulate) {
-  if (check_paged(cache, batch, 1) != LK_OK || max_seq_len < 0 ||
+  if (check_paged(cache, batch, 1) != LK_OK || max_seq_len < 0 || max_seq_len > kMaxSlots ||
       check_decode_heads(cache, batch, n_heads, max_seq_len) != LK_OK)
     return 0;
   return lk::paged_decode_workspace_bytes(batch, cache->n_kv_heads, n_heads, cache->head_dim, cache->dtype,
@@ -207,7 +209,7 @@ lk_status lk_paged_decode_attn(const lk_paged_cache* cache, const int32_t* page_
 
 size_t lk_paged_evict_workspace_bytes(const lk_paged_cache* cache, int32_t batch, int32_t max_seq_len,
                                       int32_t budget) {
-  if (check_paged(cache, batch, 1) != LK_OK || max_seq_len < 0 || budget < 1) return 0;
+  if (check_paged(cache, batch, 1) != LK_OK || max_seq_len < 0 || max_seq_len > kMaxSlots || budget < 1) return 0;
   return lk::paged_evict_workspace_bytes(batch * cache->n_kv_heads, max_seq_len, budget);
 }
 

@@ -288,3 +288,15 @@ def test_the_binding_is_built_again_for_another_torch(L, tmp_path, monkeypatch):
     monkeypatch.setattr(importlib.util, "find_spec", lambda n, *a: None if n == "torch" else find(n, *a))
     b._build_ext(True, False)                                 # no torch: the library alone
     assert len(built) == 2
+
+
+def test_workspaces_of_sequences_longer_than_any_table(L):
+    # a table has at most 2^30 slots: no size for more, and none that wrapped around
+    m = desc(L, mass=at(2), pos=at(3))
+    for n, known in ((1 << 30, True), ((1 << 30) + 1, False), (2 ** 31 - 1, False)):
+        sizes = [L.lib.lk_paged_decode_workspace_bytes(C.byref(m), 2, 4, n, acc) for acc in (0, 1)]
+        sizes.append(L.lib.lk_paged_evict_workspace_bytes(C.byref(m), 2, n, 64))
+        assert all((s > 0) == known for s in sizes), (n, sizes)
+    # scores of 2^30 slots; keys and bits of as many for eviction
+    assert L.lib.lk_paged_decode_workspace_bytes(C.byref(m), 2, 4, 1 << 30, 1) >= 2 * 4 * 2 ** 30 * 4
+    assert L.lib.lk_paged_evict_workspace_bytes(C.byref(m), 2, 1 << 30, 64) >= 4 * 2 ** 30 * 4
