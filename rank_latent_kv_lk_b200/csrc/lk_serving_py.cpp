@@ -143,6 +143,11 @@ struct PagedCache {
   }
 };
 
+// Scratch of a call over a page table; none for lengths beyond it, which the library then refuses.
+Tensor scratch_for(size_t bytes, int32_t max_seq_len, int32_t width, const PagedCache& c) {
+  return scratch(max_seq_len <= (int64_t)width * c.d.page_size ? bytes : 0, c.dev);
+}
+
 int32_t as_i32(const char* name, int64_t v) {
   TORCH_CHECK_VALUE(v >= INT32_MIN && v <= INT32_MAX, name, ": ", v, " does not fit in 32 bits");
   return (int32_t)v;
@@ -190,7 +195,7 @@ Tensor paged_decode_attn(PagedCache& c, const Tensor& table, const Tensor& q, co
   const int32_t b = as_i32("batch", batch), h = as_i32("n_heads", heads), m = as_i32("max_seq_len", max_seq_len);
   if (b == 0) return o;
   const size_t need = lk_paged_decode_workspace_bytes(&c.d, b, h, m, accumulate);
-  const Tensor ws = scratch(need, c.dev);
+  const Tensor ws = scratch_for(need, m, width, c);
   check(lk_paged_decode_attn(&c.d, ptr<int32_t>(table), b, width, ptr(q), qt, h,
                              as_i32("stride of q", batch > 1 ? q.stride(0) : heads * dim), ptr<int32_t>(seq_len), m,
                              (float)softmax_scale.value_or(1.0 / std::sqrt((double)dim)), accumulate, ptr(o), ot,
@@ -216,7 +221,7 @@ void paged_evict(PagedCache& c, const Tensor& table, const Tensor& seq_len, cons
   const int32_t b = as_i32("batch", batch), m = as_i32("max_seq_len", max_seq_len), n = as_i32("budget", budget);
   if (b == 0) return;
   const size_t need = lk_paged_evict_workspace_bytes(&c.d, b, m, n);
-  const Tensor ws = scratch(need, c.dev);
+  const Tensor ws = scratch_for(need, m, width, c);
   check(lk_paged_evict(&c.d, ptr<int32_t>(table), b, width, ptr<int32_t>(seq_len), ptr<int32_t>(next_pos), m, n,
                        as_i32("window", window), as_i32("n_sink", n_sink),
                        mass_out ? ptr<float>(mass_out) : ptr<float>(c.mass),

@@ -341,3 +341,22 @@ def test_no_sequences():
     with pytest.raises(ValueError):
         lk.paged_decode_attn(layer.cache, table, q[:, :, :16], n, 64)
     assert torch.equal(before[0], layer.cache.k) and torch.equal(before[1], layer.cache.mass)
+
+
+def test_a_refused_length_allocates_nothing():
+    # scratch for 2^24 slots would be gigabytes
+    import rank_latent_kv_lk_b200 as lk
+    cache = lk.PagedKVCache(8, 16, 2, 64, mass=True)
+    table = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    seq = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, 4, 64, dtype=BF, device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    for call in (lambda n: lk.paged_decode_attn(cache, table, q, seq, n, accumulate=True),
+                 lambda n: lk.paged_evict(cache, table, seq, seq.clone(), n, 8)):
+        for n in (65, 1 << 24, 2 ** 31 - 1):
+            with pytest.raises(lk.LkError):
+                call(n)
+        with pytest.raises(ValueError):
+            call(1 << 31)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 20
