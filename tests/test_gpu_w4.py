@@ -112,3 +112,37 @@ def test_infinities_stay_in_their_row():
     want, mag = product(x[[0, 2]], codes, scales, 128)
     check(y[[0, 2]], want, bound(128) * mag + 1e-30, "other rows")
     assert not torch.isfinite(y[1][dense(codes, scales, 128)[:, 5] != 0]).any()
+
+
+# More tiles of 16 outputs than the GPU has SMs (148): several a CTA, whose warps share the staged rows of x.  The tiles
+# are no multiple of a CTA's in most, the outputs no multiple of 16, the inputs end inside a step of 128, and the steps
+# go round the ring or are fewer than its stages.
+WIDE = [(2400, 160, 32), (2369, 64, 64), (4090, 192, 64), (4096, 1184, 32), (7000, 384, 128), (9473, 288, 32),
+        (11003, 320, 64), (11008, 896, 128), (20001, 160, 32)]
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("m", [1, 5, 16, 32, 33])
+@pytest.mark.parametrize("size", WIDE, ids=[str(s) for s in WIDE])
+def test_several_tiles_a_cta(size, m, dt):
+    import rank_latent_kv_lk_b200 as lk
+    n, k, group = size
+    g = torch.Generator().manual_seed(n + m)
+    one, two = weights(n, k, group, g), weights(n, k, group, g)
+    x = torch.randn(m, k, generator=g).to(dt)
+    a, am = product(x, *one, group)
+    b, bm = product(x, *two, group)
+    da, db = bound(k) * am, bound(k) * bm
+    w = lk.W4Weight(one[0].cuda(), one[1].cuda())
+    check(lk.w4_linear(w, x.cuda(), y_dtype=F32), a, da + 1e-30, "linear")
+    res = torch.randn(m, n, generator=g).to(dt)
+    both = a + res.to(F64)
+    check(lk.w4_linear(w, x.cuda(), residual=res.cuda()), both,
+          da + (HALF_STEP[dt] + 2.0 ** -24) * (both.abs() + da) + 2.0 ** -25, "residual")
+    w = lk.W4Weight(one[0].cuda(), one[1].cuda(), two[0].cuda(), two[1].cuda())
+    want = a * torch.sigmoid(a) * b
+    tol = 1.1 * da * (b.abs() + db) + (a * torch.sigmoid(a)).abs() * db + 8 * 2.0 ** -23 * want.abs() + 1e-30
+    got = lk.w4_linear(w, x.cuda(), y_dtype=F32)
+    check(got, want, tol, "gated")
+    for _ in range(5):
+        assert torch.equal(lk.w4_linear(w, x.cuda(), y_dtype=F32), got)
