@@ -263,3 +263,54 @@ def test_tensors_of_a_cache_and_a_weight():
     w.packed.resize_(16)
     with pytest.raises(ValueError):
         lk.w4_linear(w, torch.zeros(1, 64, dtype=BF, device="cuda"))
+
+
+# 1025 to 4096 slots: the selecting kernel of 512 threads; lens, kv heads, dim, page, dtype, budget, window, sinks
+MIDDLE = [
+    ([1025, 900, 3], 2, 32, 16, BF, 900, 16, 4),       # 125 rows can move: one launch beside the lengths
+    ([2112, 2049], 2, 64, 64, HF, 2048, 128, 4),
+    ([4096, 4095, 0], 1, 16, 32, I8, 3900, 64, 0),
+    ([1025], 1, 128, 2, BF, 300, 20, 4),               # many rows move
+    ([4096, 1500], 2, 32, 128, HF, 1000, 64, 4),
+    ([3000], 1, 48, 16, I8, 1400, 0, 0),
+    ([2112, 700], 1, 16, 16, BF, 500, 900, 30),        # more protected than the budget
+    ([4000, 4000], 1, 16, 1, BF, 3990, 4000, 2),
+]
+
+
+@pytest.mark.parametrize("case", MIDDLE, ids=[str(i) for i in range(len(MIDDLE))])
+@pytest.mark.parametrize("kind", ["random", "ties", "special"])
+def test_evict_sequences_of_middle_length(case, kind):
+    test_evict_in_place(case, kind)
+
+
+@pytest.mark.parametrize("case", MIDDLE, ids=[str(i) for i in range(len(MIDDLE))])
+@pytest.mark.parametrize("kind", ["random", "ties"])
+@pytest.mark.parametrize("lengths_apart", [False, True])
+def test_evict_sequences_of_middle_length_into_outputs_apart(case, kind, lengths_apart):
+    import rank_latent_kv_lk_b200 as lk
+    lens, hk, dim, page, dt, budget, window, sinks = case
+    pages = Pages(lens, hk, dim, page, dt, seed=budget + 1, mass=True)
+    if kind == "ties":
+        pages.mass = torch.where(pages.live, (pages.mass * 3).floor(), pages.mass)
+    want = expect(pages, lens, budget, window, sinks)
+    cache, seq = pages.cuda(), pages.seq()
+    m, p = torch.full_like(cache.mass, -1), torch.full_like(cache.pos, -1)
+    out = torch.full_like(seq, -1) if lengths_apart else seq
+    lk.paged_evict(cache, pages.table.cuda(), seq, seq.clone(), max(lens), budget, window=window, n_sink=sinks,
+                   mass_out=m, pos_out=p, seq_len_out=out)
+    lk.device_status()
+    assert out.tolist() == [min(n, budget) for n in lens]
+    if lengths_apart:
+        assert seq.tolist() == lens
+    assert torch.equal(cache.mass.cpu().nan_to_num(9), pages.mass.nan_to_num(9))
+    assert torch.equal(cache.pos.cpu(), pages.pos)
+    for n in [x for x in want if x not in ("mass", "pos")]:
+        torch.testing.assert_close(getattr(cache, n).cpu(), want[n], rtol=0, atol=0, equal_nan=True, msg=n)
+    kept = torch.zeros_like(pages.live)
+    for b, n in enumerate(lens):
+        for t in range(min(n, budget)):
+            kept[pages.table[b, t // page], :, t % page] = True
+    for got, n in ((m.cpu(), "mass"), (p.cpu(), "pos")):
+        assert torch.equal(got[kept], want[n][kept]), n
+        assert (got[~kept] == -1).all(), n
