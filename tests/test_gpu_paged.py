@@ -305,3 +305,18 @@ def test_fp32_outputs_of_a_bf16_cache_keep_fp32_weights(lens):
             w = math.exp(-float(q[b, h, 0]))
             want[b, h] = w / (1 + w) * pages.dense(b, h // 4)[1][1]
     check(got, want, 6 * 2.0 ** -22 * want.abs() + 1e-30, "fp32 out")
+
+
+MORE_WEIGHTS = [c for i, c in enumerate(CASES) if i % 3 != 2] + [
+    # int8 and fp16 through the split and the join: one chunk of heads, two, an odd end, an empty sequence
+    ([2000, 700], 1, 20, 128, 32, I8, BF),
+    ([1100, 0, 531], 2, 11, 192, 16, I8, HF),
+    ([3000, 1], 1, 40, 64, 64, I8, BF),
+    ([2500, 513], 1, 17, 80, 4, HF, HF),
+    ([5000], 1, 9, 256, 128, BF, BF),
+]
+
+
+@pytest.mark.parametrize("case", MORE_WEIGHTS, ids=[str(i) for i in range(len(MORE_WEIGHTS))])
+def test_accumulated_weight_of_the_other_cases(case):
+    test_accumulated_weight(case)
