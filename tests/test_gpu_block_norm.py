@@ -123,3 +123,27 @@ def test_nan_and_infinity_stay_in_their_row():
     y[1, 3] = float("nan")
     x, h = lk.rmsnorm_gate_residual(y, y.nan_to_num(), w_post=w, w_pre=w)
     assert torch.isfinite(h[[0, 2]]).all() and torch.isnan(h[1]).all()
+
+
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+@pytest.mark.parametrize("pre", [False, True])
+@pytest.mark.parametrize("dt", [BF, HF, F32])
+def test_parts_of_long_rows(dt, post, gate, pre):
+    # odd widths in whole vectors, and two vectors a thread (256 rows and more)
+    for m, width in ((3, 2049), (2, 4099), (5, 2054), (2, 16387), (300, 4096), (257, 1032)):
+        run(m, width, dt, post, gate, pre, seed=m)
+
+
+@pytest.mark.parametrize("xo,ho", [("x", "y"), ("y", None), ("x", None)])
+@pytest.mark.parametrize("m,width", [(7, 2049), (4, 4099), (6, 2054), (300, 4096), (257, 1032), (1100, 1001)])
+def test_long_rows_in_place(m, width, xo, ho):
+    import rank_latent_kv_lk_b200 as lk
+    g = torch.Generator().manual_seed(1)
+    for dt in (BF, HF, F32):
+        y, x, gate, w = (torch.randn(*s, generator=g).to(dt).cuda() for s in (*[(m, width)] * 3, (width,)))
+        want = lk.rmsnorm_gate_residual(y, x, w_post=w, gate=gate, w_pre=w)
+        t = dict(x=x.clone(), y=y.clone())
+        got = lk.rmsnorm_gate_residual(t["y"], t["x"], w_post=w, gate=gate, w_pre=w, x_out=t[xo], h=t.get(ho))
+        assert got[0].data_ptr() == t[xo].data_ptr()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
