@@ -55,7 +55,8 @@ typedef enum {
   LK_ERR_UNSUPPORTED = 6, /* valid request the library does not implement   */
   LK_ERR_WORKSPACE = 7,   /* workspace null or smaller than required        */
   LK_ERR_CUDA = 8,        /* a CUDA call failed (text in lk_last_error)     */
-  LK_ERR_DEVICE = 9       /* a kernel reported a bounded wait that expired  */
+  LK_ERR_DEVICE = 9       /* a kernel reported a bounded wait that expired, or
+                             a page or length outside its paged cache       */
 } lk_status;
 
 typedef enum {
@@ -481,7 +482,9 @@ lk_status lk_debug_decode_attn_stall(const lk_latent_cache* k_cache, const lk_la
                                      int32_t stall_item, uint32_t wait_us, lk_stream_t stream);
 
 /* Synchronises the device, then reports (and with reset != 0 clears) the
- * error word kernels set when a bounded wait expires: LK_OK or LK_ERR_DEVICE. */
+ * error word that kernels of the current device set when a bounded wait
+ * expires or a page or length lies outside its paged cache (lk_serving.h):
+ * LK_OK or LK_ERR_DEVICE. */
 lk_status lk_device_status(int32_t reset);
 
 const char* lk_status_string(lk_status status);

@@ -336,7 +336,8 @@ def swiglu_quant_i8(gate, up, stream=None):
 
 
 def device_status(reset=True):
-    """Synchronise and raise if a kernel reported an expired bounded wait."""
+    """Synchronise the current device and raise if one of its kernels reported an expired bounded wait, or a page or
+    length outside its paged cache."""
     check(lib.lk_device_status(1 if reset else 0))
 
 
