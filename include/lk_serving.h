@@ -40,7 +40,7 @@ extern "C" {
  * mass, eviction) must belong to one sequence and be listed once.  The host
  * cannot check page ids: a kernel that meets one outside [0, n_pages) skips its
  * slots (not attended, written or moved) and lk_device_status() reports
- * LK_ERR_DEVICE.
+ * LK_ERR_DEVICE.  batch is at least 1 in every call.
  */
 typedef struct {
   int32_t n_pages, page_size, n_kv_heads, head_dim;
@@ -96,13 +96,16 @@ lk_status lk_paged_append(const lk_paged_cache* cache, const int32_t* page_table
  * Scores, softmax statistics and the output sum are fp32; the weights p meet
  *   V as a sum of two 16-bit terms (relative rounding at most 2^-16, fp16 and
  *   int8 caches 2^-22 but not below 2^-35 of their sum), for an LK_F32 out of a
- *   bf16 cache of three (2^-24).
+ *   bf16 cache of three (2^-24).  An int8 cache's weights carry their V row's
+ *   scale, relative to a power of two of at most twice the largest attended
+ *   one: beside a row whose v_scale is 2^35 times theirs, others vanish.
  *   Weights are held at up to 2^4 (fp16 and int8 caches: 2^14), and that times
  *   seq_len |v| has to stay in fp32's range; an infinity in an attended V row
  *   makes its dim NaN.
  *   Results do not depend on timing.  One launch for a max_seq_len of up to
- *   512 (for accumulate: and a group of at most 8 heads, 16 up to head_dim
- *   128), else two.
+ *   512, or up to min(2048, 24 units) where that is more, else two; a unit is a
+ *   sequence, a kv head and up to 8 heads of its group (16 of a larger group up
+ *   to head_dim 128).  accumulate: one launch only where the group is one unit.
  */
 lk_status lk_paged_decode_attn(const lk_paged_cache* cache, const int32_t* page_table, int32_t batch,
                                int32_t table_width, const void* q, lk_dtype q_dtype, int32_t n_heads,
@@ -165,8 +168,9 @@ size_t lk_w4_packed_bytes(int32_t n_out, int32_t k_in, int32_t group, int32_t ga
  *   8); y: [m, n_out] LK_BF16, LK_F16 or LK_F32, contiguous; residual: NULL or
  *   [m, n_out] of x_dtype, contiguous (may be y if the types are the same);
  *   not with a gated weight.
- * Codes and x enter exact products; sums and scales are fp32; one rounding to
- * y's type.
+ * Codes and x enter exact products; sums and scales are fp32 (8 |x| summed over
+ * a group, before its scale, has to stay in fp32's range); one rounding to y's
+ * type.
  */
 lk_status lk_w4_linear(const void* packed, int32_t n_out, int32_t k_in, int32_t group, int32_t gated,
                        const void* x, lk_dtype x_dtype, int32_t m, int32_t x_stride, const void* residual,
@@ -180,8 +184,8 @@ lk_status lk_w4_linear(const void* packed, int32_t n_out, int32_t k_in, int32_t 
  * `dtype` (LK_BF16, LK_F16 or LK_F32), contiguous.  w_post NULL: y enters as it
  * is; gate NULL: 1; gate_per_row 0: [width], 1: [m, width]; w_pre and h both
  * NULL: no second norm.  Weights and gate of `dtype`.  x_out may be x or y, h
- * may be y.  Everything is fp32 inside; h is taken from x_out before its
- * rounding.  width <= 32768.
+ * may be y.  Everything is fp32 inside (a row's sum of squares has to stay in
+ * its range); h is taken from x_out before its rounding.  width <= 32768.
  */
 lk_status lk_rmsnorm_gate_residual(const void* y, const void* x, const void* w_post, const void* gate,
                                    int32_t gate_per_row, const void* w_pre, lk_dtype dtype, int32_t m,

@@ -128,7 +128,9 @@ def paged_decode_attn(cache, page_table, q, seq_len, max_seq_len, softmax_scale=
     q: [batch, n_heads, head_dim], heads contiguous within a sequence, n_heads a
     multiple of the cache's kv heads; seq_len: device int32 [batch];
     max_seq_len: host bound.  accumulate: add every cached token's attention
-    weight, summed over the heads of its group, to cache.mass.
+    weight, summed over the heads of its group, to cache.mass.  out: where the
+    result goes, in its own type; without it, a new tensor of out_dtype
+    (default: q's).
     """
     if stream is not None:
         return _on(stream, cache.device, paged_decode_attn, cache, page_table, q, seq_len, max_seq_len, softmax_scale,
@@ -174,6 +176,8 @@ def w4_linear(w, x, residual=None, y=None, y_dtype=None, stream=None):
     """x W^T (+ residual), or silu(x gate^T) * (x up^T) for a gated weight.
 
     x: [m, k_in] bf16 or fp16, rows contiguous; residual: [m, n_out] of x's type.
+    y: where the result goes, in its own type; without it, a new tensor of
+    y_dtype (default: x's).
     """
     if stream is not None:
         return _on(stream, w.packed.device, w4_linear, w, x, residual, y, y_dtype)
