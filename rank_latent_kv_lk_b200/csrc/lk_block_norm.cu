@@ -1,8 +1,9 @@
 // The norms around a block with its gate and residual scale (sm_100a):
 //   x_out = x + scale * gate . (RMSNorm(y) . w_post),  h = RMSNorm(x_out) . w_pre
 // HBM-bound: y, x (and a gate per row) are read once, x_out and h written once
-// (4096 rows of 4096, fp16, gate per row: 168 MB in 26.8 us, 97 % of the
-// measured copy bandwidth; 32 rows: 2.2 us, the latency of one row).
+// (4096 rows of 4096, fp16, gate per row, 168 MB: 28.9 us a call, 90 % of the
+// measured copy bandwidth, 26.8 in a captured graph; 32 rows: 5.6 us a call, the
+// host's part of it, 2.2 in a graph, the latency of one row).
 // One CTA per row: a thread keeps its elements of the row in registers between
 // the two block-wide sums of squares, so nothing is read twice, and the row is
 // read whole before any of it is written (x_out may be x or y, h may be y).
@@ -355,8 +356,10 @@ cudaError_t launch_v(const NormParams& p, int m, cudaStream_t stream) {
   const bool all = ok(p.y) && ok(p.x) && ok(p.w_post) && ok(p.gate) && ok(p.w_pre) && ok(p.x_out) && ok(p.h);
   if (!all) return launch_t<T, 1>(p, m, stream);
   if (p.width % V == 0) return launch_t<T, V>(p, m, stream);
-  // Cut vectors pay from some width or size on (fp16: 6 rows of 1292 3.5 us against 2.2 element by element, 10 of
-  // 5580 3.5 against 4.2, 2706 of 2156 12.6 against 29.5).
+  // Cut vectors pay from some width or size on.  In a graph, against element by element, fp16: 64 rows of 1023 3.3 us
+  // against 1.9, of 2051 3.4 against 2.7, of 4099 3.6 against 4.2, of 8197 6.0 against 11.6; 256 of 2051 3.6 against
+  // 4.0; 1024 of 515 3.7 against 3.3, of 1023 6.0 against 5.1, of 1541 6.1 against 8.3; 4096 of 1023 12.5 against 17.0.
+  // fp32: 64 rows of 2051 2.8 against 2.6, of 8197 7.2 against 12.1; 1024 of 1023 4.7 against 5.0.
   return p.width >= 2048 || (int64_t)m * p.width >= 1 << 20 ? launch_odd<T, V>(p, m, stream)
                                                             : launch_t<T, 1>(p, m, stream);
 }

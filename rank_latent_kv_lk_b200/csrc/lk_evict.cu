@@ -15,13 +15,16 @@
 // a whole; the first bins are counted as the keys are made.  Which slots stay becomes a bit each;
 // a thread then takes a word of 32, and prefix sums over the threads number
 // the equal keys (ties go to the lowest slots), the holes and the moving
-// tokens.  The CTA also writes the kept mass and positions.  Bound by
-// instructions and latency: hence four tokens an access, and no look at ties
-// where there are none.  Clusters did not pay: eight CTAs a unit, their bins
-// summed over distributed shared memory, took 98 us for 16384 tokens a unit
-// where one took 36; a pair gained 3 %.  With the moves: 32 x 8 units
-// from 2112 to 2048 slots 10.9 us, 8 x 8 of up to 16384 to 4096 40.1 us (20 of
-// them the rows' bytes both ways, near the copy bandwidth).
+// tokens.  The CTA also writes the kept mass and positions.  Bound by latency,
+// a chain of block-wide steps (schedulers issue in 39 to 46 % of their cycles,
+// barriers and loads are what warps wait for most): hence four tokens an
+// access, and no look at ties where there are none.  A cluster of eight CTAs a
+// unit that each read all the others' bins over distributed shared memory took
+// 98 us for 16384 tokens a unit where one CTA took 36, a pair gained 3 %; one
+// whose CTAs each sum a part of the bins was not built.  With the moves, a call
+// (in a captured graph): 32 x 8 units from 2112 to 2048 slots 10.8 us (11.1),
+// 8 x 8 of up to 16384 to 4096 41.2 us (40.1), 20 of them the rows' bytes both
+// ways, near the copy bandwidth, and 20 with 64 of the SMs at work.
 // move_kernel: the listed rows of K and V (and int8 scales), 16 bytes a lane,
 // and the new lengths (which select_kernel's CTAs still read).  Where few rows
 // can move, select_kernel moves them itself.

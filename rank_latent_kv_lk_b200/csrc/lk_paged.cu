@@ -5,9 +5,11 @@
 //   s_t = scale q_j . k_t,  p = softmax(s),  out_j = sum_t p_t v_t,
 //   and with accumulate  mass_t += sum_j p_t.
 // HBM-bound: every K and V row is read once (2 D element bytes a token and kv
-// head against 4 D flops a head of the group).  bf16, D = 128: 8 ragged
-// sequences to 16384, group 4, 52.7 us, 80 % of the measured copy bandwidth;
-// one of 4224, 32 kv heads, 20.4 us (53 %: two launches and the ramp).
+// head against 4 D flops a head of the group).  bf16, D = 128, a call (in a
+// captured graph): 8 ragged sequences to 16384, group 4, 53.9 us (53.0), 78 %
+// of the measured copy bandwidth; one of 4224, 32 kv heads, 21.0 us (20.3),
+// 51 %: two launches and the ramp, schedulers issue in 23 % of their cycles and
+// wait for memory otherwise.
 //
 // Split.  A unit is (sequence, kv head, chunk of up to 8 NT heads of its
 // group); a unit's tokens are cut into blocks of 16, and the blocks of all
@@ -42,8 +44,9 @@
 // weight is 2^14, the sum at least 2^10 and the smallest step 2^-24.
 // int8 caches: codes are exact in fp16 (byte permute into the mantissa of
 // 1024, one exact subtract); bf16 queries are first scaled by a power of two
-// per head so that the largest lies in [2^14, 2^15) (values below 2^-39 of
-// it round, which fp32 sums do not show); V weights are p times the token's
+// per head so that the largest lies in [2^14, 2^15) (values below about 2^-31
+// of it meet fp16's smallest step and are off by up to 2^-39 of the largest,
+// which fp32 sums do not show); V weights are p times the token's
 // scale over a running power of two, so that they too stay at most 2^14.
 //
 // Masked slots (behind the length, or on a page outside the pool) are not
@@ -1116,10 +1119,13 @@ int log2_of(int x) {
 // accumulators of 16 heads still fit.
 int heads_per_chunk(int group, int D) { return group > 8 && D <= 128 ? 16 : 8; }
 
-// Up to so many tokens (more with more units, which share the GPU) a unit is one CTA's: one launch and no join.
-// 256-byte rows, direct against split: 4 units of 512 tokens 7.7 us against 8.0, of 768 tokens 9.7 against 8.4;
-// 32 units of 768 tokens 9.9 against 9.7; 128 units of 1024 tokens 15.2 against 22.0, of 2048 24.9 against 32.3;
-// 256 units of 1024 tokens 25.4 against 30.9.  Equal lengths; where they differ the split gains.
+// Up to so many tokens (more with more units, which share the GPU) a unit is one CTA's: one launch and no join.  The
+// lengths are the device's, so the rule knows only their bound.  256-byte rows, group 4, in a graph, direct against
+// split: equal lengths: 4 units of 512 tokens 6.7 us against 7.9; 32 of 768 8.4 against 10.7; 128 of 1024 14.2 against
+// 21.1, of 2048 23.8 against 31.2; 256 of 2048 50.5 against 50.7.  Lengths spread over (0, max]: 128 units to 1024
+// 11.6 against 27.5, to 2048 18.2 against 30.7, 256 to 2048 32.4 against 43.7.  The split gains where one sequence is
+// much longer than all others (64 tokens): 128 units, one sequence of 1024 9.9 against 10.5, of 2048 15.9 against
+// 13.0; 256 units, of 2048 23.6 against 15.8.
 constexpr int kDirect = 512, kDirectPer = 24, kDirectMost = 2048;
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }

@@ -3,10 +3,13 @@
 //   y[m, n] = sum_g s[n, g] sum_{k in g} c[n, k] x[m, k]  (+ residual), or
 //   silu(y_gate) * y_up for a gated weight.
 // The floor is the weights' bytes (n k / 2 of codes and 2 n k / group of
-// scales) up to the 32 rows of one pass; what bounds it is issue slots (the
-// expansion of the codes), and with 32 rows the warp-level products.  bf16, one
-// row, 4096 x 4096 4.4 us; one row, SwiGLU, 2 x 11008 x 4096 12.5 us, 4.1 TB/s;
-// 32 rows of the same 28.0 us.
+// scales) up to the 32 rows of one pass.  No one unit is full: one row,
+// SwiGLU, 2 x 11008 x 4096 12.6 us a call, 4.0 TB/s: schedulers issue in 56 % of
+// the cycles (most of it the expansion of the codes) at 23 % of the warps an SM
+// holds; eight rows, 4096 x 11008 11.1 us: the same 56 %, every CTA copies all
+// of x, as many bytes as its weights, and 20 SMs have no CTA; 32 rows of the
+// first 28.0 us: warps wait most for the tensor and arithmetic pipes.  bf16, one
+// row, 4096 x 4096 4.7 us a call, 4.2 in a captured graph.
 //
 // Layout (lk_w4_pack).  A tile is 16 outputs x 64 inputs: one 16-byte word
 // group per lane, in the order of the operand A of four m16n8k16 products, so
