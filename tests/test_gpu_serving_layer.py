@@ -360,3 +360,32 @@ def test_a_refused_length_allocates_nothing():
         with pytest.raises(ValueError):
             call(1 << 31)
     assert torch.cuda.max_memory_allocated() - before < 1 << 20
+
+
+def test_a_side_stream_inside_a_capture():
+    # stream= on a stream that forks from the captured one and joins it again
+    import rank_latent_kv_lk_b200 as lk
+    g = torch.Generator().manual_seed(4)
+    w = lk.W4Weight(*(t.cuda() for t in w4(512, 256, g)))
+    x, one = torch.randn(4, 256, generator=g).to(BF).cuda(), torch.ones(512, dtype=BF, device="cuda")
+
+    def both(x, side, here):
+        y = x + 1
+        side.wait_stream(here)
+        a = lk.w4_linear(w, y, stream=side)
+        del y
+        b = lk.w4_linear(w, x)
+        here.wait_stream(side)
+        return lk.rmsnorm_gate_residual(a, b, w_pre=one)
+
+    here = torch.cuda.current_stream()
+    both(x, torch.cuda.Stream(), here)
+    graph, sx = torch.cuda.CUDAGraph(), x.clone()
+    with torch.cuda.graph(graph):
+        out = both(sx, torch.cuda.Stream(), torch.cuda.current_stream())
+    for scale in (1.0, -2.0, 0.5):
+        sx.copy_(x * scale)
+        graph.replay()
+        want = both(x * scale, torch.cuda.Stream(), here)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
