@@ -147,3 +147,31 @@ def test_long_rows_in_place(m, width, xo, ho):
         got = lk.rmsnorm_gate_residual(t["y"], t["x"], w_post=w, gate=gate, w_pre=w, x_out=t[xo], h=t.get(ho))
         assert got[0].data_ptr() == t[xo].data_ptr()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_beyond_32_bits_of_elements():
+    # The last rows of 2^31 elements and more: what those rows give alone, and float64's with the bounds of run().  (Rows
+    # of an odd width start at another element of a vector than a copy of them does, and sum in another order: those
+    # are held against float64 only.)
+    import rank_latent_kv_lk_b200 as lk
+    for width in (32768, 32749):
+        m = 2 ** 31 // width + 9
+        y, x = (torch.zeros(m, width, dtype=BF, device="cuda") for _ in range(2))
+        y[-5:].normal_()
+        x[-5:].normal_()
+        w = torch.ones(width, dtype=BF, device="cuda")
+        one = torch.ones(width, dtype=BF)
+        X, H, add = reference(y[-5:].cpu(), x[-5:].cpu(), one, None, 1.0, one, EPS)
+        alone = lk.rmsnorm_gate_residual(y[-5:].clone(), x[-5:].clone(), w_post=w, w_pre=w)
+        got = lk.rmsnorm_gate_residual(y, x, w_post=w, w_pre=w, x_out=x, h=y)
+        if width % 8 == 0:
+            assert torch.equal(got[0][-5:], alone[0]) and torch.equal(got[1][-5:], alone[1])
+        rel = (width / 2 + 10) * 2.0 ** -24
+        slack = rel * add.abs() + 2.0 ** -24 * X.abs()
+        check(got[0][-5:], X, slack, BF, "x")
+        rms = torch.sqrt((X * X).mean(-1, keepdim=True) + EPS)
+        check(got[1][-5:], H, slack / rms + (rel + slack.square().mean(-1, keepdim=True).sqrt() / rms) * H.abs(), BF,
+              "h")
+        assert (got[0][:-5].view(torch.int16) == 0).all()
+        del y, x, got
+    torch.cuda.empty_cache()

@@ -320,3 +320,35 @@ MORE_WEIGHTS = [c for i, c in enumerate(CASES) if i % 3 != 2] + [
 @pytest.mark.parametrize("case", MORE_WEIGHTS, ids=[str(i) for i in range(len(MORE_WEIGHTS))])
 def test_accumulated_weight_of_the_other_cases(case):
     test_accumulated_weight(case)
+
+
+@pytest.mark.parametrize("dt", [BF, I8])
+def test_rows_beyond_32_bits_of_bytes(dt):
+    # the last pages of pools of 8.6 GB each, through append, attention and eviction: the same as on a small pool
+    import rank_latent_kv_lk_b200 as lk
+    dim, page, hk = 256, 64, 2
+    big = 2 ** 33 // (dim * dt.itemsize * page * hk) + 7
+    got = []
+    for n_pages in (24, big):
+        g = torch.Generator().manual_seed(5)
+        shape = (n_pages, hk, page, dim)
+        k, v = (torch.empty(shape, dtype=dt, device="cuda") for _ in range(2))
+        rows = [torch.zeros(shape[:3], dtype=t, device="cuda") for t in (torch.float32, torch.int32)]
+        sc = [torch.zeros(shape[:3], device="cuda") for _ in range(2)] if dt is I8 else [None, None]
+        cache = lk.PagedKVCache.from_tensors(k, v, *sc, *rows)
+        table = (n_pages - 24 + torch.randperm(24, generator=g)).to(torch.int32).view(2, 12).cuda()
+        seq, nxt = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+        kn, vn = torch.randn(2, 2, 700, hk, dim, generator=g).to(BF).cuda()
+        q = torch.randn(2, 8, dim, generator=g).to(BF).cuda()
+        lk.paged_append(cache, table, kn, vn, seq, nxt)
+        out = [lk.paged_decode_attn(cache, table, q, seq, 768, accumulate=True)]
+        lk.paged_evict(cache, table, seq, nxt, 768, 320, window=32)
+        out.append(lk.paged_decode_attn(cache, table, q, seq, 320))
+        lk.device_status()
+        assert seq.tolist() == [320, 320]
+        ids = table[:, :5].long()
+        got.append(out + [t[ids].clone() for t in (cache.k, cache.v, cache.mass, cache.pos)])
+        del cache, k, v
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    torch.cuda.empty_cache()
