@@ -37,7 +37,8 @@
 // dims of two tokens, whose even and odd bytes are the rows of one product.
 // The weights are split into two 16-bit terms (high and remainder), so their
 // rounding is 2^-16 (bf16) or 2^-22 (fp16) relative.  An fp32 output of a bf16
-// cache gets a third term (2^-24); a 16-bit one would round it away: its error
+// cache gets a third term (2^-24) for 2 to 5 % of the time (ragged to 16384
+// 53.9 us in a graph against 52.7); a 16-bit one would round it away: its error
 // against 64 bits is the same without (relative 1.68e-3 in 2-norm, 9.5e-7 of
 // it from the two terms).  fp16 weights are held
 // 2^10 times larger, which keeps small ones out of the subnormals: the largest
